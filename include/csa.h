@@ -614,6 +614,148 @@ csa_status csa_cp_pack_rows(const void* kv_local, int E_cap_local, int E_local, 
                             int c, int kv_dtype, const int32_t* idx, const int32_t* count, int b,
                             int k, void* rows, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Serving a chunk of new tokens over a paged latent cache                   */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * A serving step brings every sequence a chunk of new tokens: one (decode), a few
+ * (drafted tokens to verify) or many (a piece of a prompt).  The calls below are such a
+ * step's parts around the compressor, the indexer and the top-k:
+ *
+ *   csa_qk_norm_rope    the query heads and the token's latent row, normalised and rotated;
+ *   csa_cache_write     compressed entries into their pages, quantised if the cache is;
+ *   csa_chunk_attn      attention of the chunk over the pages and the sliding window;
+ *   csa_window_append   the chunk's latent rows into the window rings, after the attention;
+ *   csa_cache_read      rows of a paged cache back as plain rows.
+ *
+ * Ragged batches: the rows of all sequences lie one after another, sequence s owning rows
+ * cu[s] .. cu[s+1] - 1 (cu [b+1] int32, ascending, cu[0] = 0).  The row count that a call
+ * takes (N or rows) bounds cu[b]; rows from cu[b] on are neither read nor written.  All of
+ * cu, first positions, block tables, selections and counts are device memory read by the
+ * kernels, so a captured call follows them; the host only sees the bounds.
+ */
+
+/*
+ * A paged latent cache.  Entry e of sequence s is row e % CSA_PAGE_ENTRIES of page
+ * block_table[s][e / CSA_PAGE_ENTRIES]; entries past the table, and pages outside
+ * [0, num_pages), are skipped by every call (no row there is read or written).
+ *   dtype CSA_F32 / CSA_BF16   rows [num_pages][CSA_PAGE_ENTRIES][c] elements; c a multiple
+ *                              of 8; hi and scales NULL, d_hi 0
+ *   dtype CSA_FP8_E4M3         a row's first c - d_hi dims as E4M3 codes with one power-of-two
+ *                              scale per 64 of them, its last d_hi dims (the rotary ones,
+ *                              whose error a far position would not forgive) in BF16:
+ *     rows    uint8 [num_pages][CSA_PAGE_ENTRIES][c - d_hi], c - d_hi a positive multiple of 64
+ *     hi      bf16  [num_pages][CSA_PAGE_ENTRIES][d_hi], d_hi a multiple of 16 (NULL if 0)
+ *     scales  uint8 [num_pages][CSA_PAGE_ENTRIES][S], S = (c - d_hi) / 64 rounded up to a
+ *             multiple of 8; byte g of a row is the exponent k_g + 127 of dims 64 g ..
+ *             64 g + 63, and code x stands for x * 2^k_g.  k_g is the smallest exponent with
+ *             amax <= 448 * 2^k_g, kept in [-110, 119] (a group of zeros has -110), so codes
+ *             are one exact rounding of the value and their products with the scale are
+ *             exact in BF16.  Values beyond 448 * 2^119, infinities among them, saturate;
+ *             NaN stays NaN.  The S - (c - d_hi) / 64 spare bytes are left as they are.
+ */
+typedef struct {
+  int dtype, c, d_hi;
+  int num_pages, max_pages;   /* pages in the pool; block-table row length */
+  void *rows, *hi, *scales;
+  const int32_t* block_table; /* [b][max_pages] */
+} csa_kv_cache;
+
+/*
+ * Writes ragged rows into their entries: row cu_rows[s] + j of x is entry first[s] + j of
+ * sequence s.
+ *   x         [rows] rows of kv->c elements of x_dtype (CSA_F32 or CSA_BF16), x_stride
+ *             elements apart (>= c; x_stride * element size a multiple of 16)
+ *   cu_rows   [b+1], first [b]: int32, see above
+ * Two rows must not name one entry (nor two sequences one page that both write).
+ */
+csa_status csa_cache_write(const csa_kv_cache* kv, int x_dtype, const void* x, int64_t x_stride,
+                           const int32_t* cu_rows, const int32_t* first, int b, int rows,
+                           cudaStream_t stream);
+
+/*
+ * Reads entries back as plain rows: out[s][j] is entry idx[s][j] of sequence s (entry j when
+ * idx is NULL) for j < count[s], as out_dtype (CSA_F32 or CSA_BF16); zeros for j >= count[s]
+ * and for an entry that the table or the pool does not hold.
+ *   idx [b][k] int32 or NULL; count [b] int32 or NULL (all k); out [b][k][c]
+ */
+csa_status csa_cache_read(const csa_kv_cache* kv, const int32_t* idx, const int32_t* count, int b,
+                          int k, int out_dtype, void* out, cudaStream_t stream);
+
+/*
+ * Appends a chunk's rows to the window rings: row cu_rows[s] + j of x, the row of token
+ * u = first[s] + j, goes to slot u % n_w of win[s].  Of a chunk longer than the ring only
+ * the last n_w rows are written, so no slot is written twice.
+ *   win [b][n_w][c], x [rows] rows of c elements, x_stride apart, both dtype (CSA_F32 or
+ *   CSA_BF16); c a multiple of 8
+ */
+csa_status csa_window_append(int dtype, int c, int n_w, void* win, const void* x, int64_t x_stride,
+                             const int32_t* cu_rows, const int32_t* first, int b, int rows,
+                             cudaStream_t stream);
+
+/*
+ * Normalises and rotates the query heads and the latent row of each token ("DeepSeek V4
+ * 结构速览", section "HCA（c128a 路线）": RMSNorm of every head; RoPE on the last dims):
+ *   y = x / sqrt(mean(x^2) + eps) * gain          (apply_norm; gain NULL: 1)
+ *   pairs (y[d-d_rope+2j], y[d-d_rope+2j+1]) rotated by pos * rope_theta^(-2j/d_rope),
+ *   the angle formed in float64
+ */
+typedef struct {
+  int H, d;           /* query heads; head dim = latent dim, a multiple of 8 up to 2048 */
+  int d_rope;         /* rotary dims at the end of each row; even, <= d and <= 128; 0 = none */
+  double rope_theta;
+  float eps;
+  int apply_norm;     /* 1: RMSNorm; 0: rotation only (gains must be NULL) */
+  int dtype;          /* CSA_F32 or CSA_BF16: q, kv, q_out and kv_out */
+} csa_norm_rope_params;
+
+/*
+ *   q        [N] tokens of H * d elements, q_stride elements apart, or NULL
+ *   kv       [N] rows of d elements, kv_stride elements apart, or NULL
+ *            (strides as in csa_cache_write: q and kv may lie in one projection's output)
+ *   q_gain, kv_gain  [d] float32 or NULL;  pos [N] int32
+ *   q_out    [N][H][d], kv_out [N][d]; may be the inputs themselves where those are
+ *            contiguous, and must not overlap them otherwise
+ */
+csa_status csa_qk_norm_rope(const csa_norm_rope_params* p, const void* q, int64_t q_stride,
+                            const float* q_gain, const void* kv, int64_t kv_stride,
+                            const float* kv_gain, const int32_t* pos, int N, void* q_out,
+                            void* kv_out, cudaStream_t stream);
+
+/*
+ * Attention of ragged chunks of new tokens over a paged cache: csa_sparse_attn's rows and
+ * formulas (p as there; p->dtype is the type of q, win, new_win and out), with
+ *   token i of sequence s   row cu_q[s] + i of q, at position t = pos0[s] + i
+ *   its entries             kv's entries idx[row][j], j < count[row] <= k; with idx NULL (and
+ *                           then p->k = 0) every entry below E(t) = floor((t+1)/m).  kv->c = p->d; kv->dtype is
+ *                           p->dtype, or CSA_FP8_E4M3
+ *   its window              tokens max(0, t-n_w+1) .. t: the row of token u is new_win's row
+ *                           cu_q[s] + u - pos0[s] from pos0[s] on, and slot u % n_w of win[s]
+ *                           before (the rings as csa_decode_paged and csa_window_append keep
+ *                           them, not yet holding the chunk)
+ * A token with no row at all (n_w = 0 and no entry) gets zeros, and its sink as lse.
+ *   q [N][H][d], idx [N][k] or NULL, count [N] (NULL iff idx NULL), new_win [N][d],
+ *   win [b][n_w][d] (both NULL iff n_w = 0), sink [H] (-inf: no sink), out [N][H][d],
+ *   lse [N][H] float32 or NULL
+ *   L_max  bounds t + 1 over the batch; it only sets how the work is split
+ *   ws     device scratch of csa_chunk_attn_workspace_size() bytes, 16-byte aligned (NULL
+ *          when 0), for this call alone until it has run.  The size depends on the current
+ *          device as well as on the arguments.
+ * 64 heads of 512 dims in BF16 over a BF16 cache, or an FP8 one with d_hi = 64, run on the
+ * tensor cores (d_rope_out up to 64 there); other shapes on the CUDA cores.
+ */
+csa_status csa_chunk_attn(const csa_attn_params* p, const csa_kv_cache* kv, const void* q,
+                          const int32_t* cu_q, const int32_t* pos0, const int32_t* idx,
+                          const int32_t* count, const void* win, const void* new_win,
+                          const float* sink, int b, int N, int L_max, void* out, float* lse,
+                          void* ws, size_t ws_bytes, cudaStream_t stream);
+size_t csa_chunk_attn_workspace_size(const csa_attn_params* p, const csa_kv_cache* kv, int b, int N,
+                                     int L_max);
+/* Number of kernel launches one csa_chunk_attn call makes with these arguments; host only. */
+int csa_chunk_attn_launch_count(const csa_attn_params* p, const csa_kv_cache* kv, int b, int N,
+                                int L_max);
+
 #ifdef __cplusplus
 }
 #endif

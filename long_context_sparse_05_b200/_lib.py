@@ -101,6 +101,20 @@ class PrefillTensors(ctypes.Structure):
     _fields_ = [(n, c_void_p) for n in _PREFILL_TENSORS]
 
 
+class KVCache(ctypes.Structure):
+    """csa_kv_cache; made by kv_cache(), which keeps the arrays alive."""
+    _fields_ = [("dtype", c_int), ("c", c_int), ("d_hi", c_int), ("num_pages", c_int),
+                ("max_pages", c_int), ("rows", c_void_p), ("hi", c_void_p), ("scales", c_void_p),
+                ("block_table", c_void_p)]
+
+
+class NormRopeParams(ctypes.Structure):
+    _fields_ = [("H", c_int), ("d", c_int), ("d_rope", c_int), ("rope_theta", c_double),
+                ("eps", c_float), ("apply_norm", c_int), ("dtype", c_int)]
+
+
+SCALE_GROUP = 64   # dims sharing one scale of an FP8 cache row
+
 _lib = None
 
 _SIGS = {
@@ -148,6 +162,21 @@ _SIGS = {
     "csa_cp_merge_workspace_size": (c_size_t, [c_int, c_int, c_int]),
     "csa_cp_merge": (c_int, [c_void_p, c_void_p, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p,
                              c_void_p, c_size_t, c_void_p]),
+    "csa_cache_write": (c_int, [ctypes.POINTER(KVCache), c_int, c_void_p, ctypes.c_int64, c_void_p,
+                                c_void_p, c_int, c_int, c_void_p]),
+    "csa_cache_read": (c_int, [ctypes.POINTER(KVCache), c_void_p, c_void_p, c_int, c_int, c_int,
+                               c_void_p, c_void_p]),
+    "csa_window_append": (c_int, [c_int, c_int, c_int, c_void_p, c_void_p, ctypes.c_int64, c_void_p,
+                                  c_void_p, c_int, c_int, c_void_p]),
+    "csa_qk_norm_rope": (c_int, [ctypes.POINTER(NormRopeParams), c_void_p, ctypes.c_int64, c_void_p,
+                                 c_void_p, ctypes.c_int64, c_void_p, c_void_p, c_int, c_void_p,
+                                 c_void_p, c_void_p]),
+    "csa_chunk_attn": (c_int, [ctypes.POINTER(AttnParams), ctypes.POINTER(KVCache)] +
+                       [c_void_p] * 8 + [c_int] * 3 + [c_void_p] * 3 + [c_size_t, c_void_p]),
+    "csa_chunk_attn_workspace_size": (c_size_t, [ctypes.POINTER(AttnParams),
+                                                 ctypes.POINTER(KVCache), c_int, c_int, c_int]),
+    "csa_chunk_attn_launch_count": (c_int, [ctypes.POINTER(AttnParams), ctypes.POINTER(KVCache),
+                                            c_int, c_int, c_int]),
     "csa_cp_pack_rows": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_int, c_void_p, c_void_p,
                                  c_int, c_int, c_void_p, c_void_p]),
 }
@@ -364,3 +393,158 @@ def csa_cp_pack_rows(kv_local, E_cap_local, E_local, entry_offset, c, kv_dtype, 
                      rows, stream=None):
     _check(lib().csa_cp_pack_rows(_ptr(kv_local), E_cap_local, E_local, entry_offset, c, kv_dtype,
                                   _ptr(idx), _ptr(count), b, k, _ptr(rows), _stream(stream)))
+
+
+# ---------------------------------------------------------------- chunks over a paged cache
+
+_ELEM = {CSA_F32: torch.float32, CSA_BF16: torch.bfloat16, CSA_FP8_E4M3: torch.uint8}
+
+
+def _plain(dtype):
+    """torch type of a csa_dtype of plain elements."""
+    if dtype not in (CSA_F32, CSA_BF16):
+        raise CsaError("expected CSA_F32 or CSA_BF16 (got %s)" % dtype)
+    return _ELEM[dtype]
+
+
+_BYTES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _arg(x, dtype, what, numel=None):
+    """Address of a contiguous CUDA tensor of the given type (and at least numel elements)
+    on the current device; None stays None."""
+    if x is None:
+        return None
+    p = _ptr(x)
+    if x.dtype != dtype and not (dtype is torch.uint8 and x.dtype in _BYTES):
+        raise CsaError("%s must be %s (got %s)" % (what, dtype, x.dtype))
+    if x.device.index != torch.cuda.current_device():
+        raise CsaError("%s is on %s, not on the current device" % (what, x.device))
+    if numel is not None and x.numel() < numel:
+        raise CsaError("%s holds %d elements, %d are needed" % (what, x.numel(), numel))
+    return p
+
+
+def _strided(x, dtype, n, rows, what):
+    """(address, elements between rows) of a CUDA tensor of `rows` rows of n elements whose
+    first dimension may be strided."""
+    if x is None:
+        return None, 0
+    if x.device.type != "cuda":
+        raise CsaError("tensor arguments must be CUDA tensors (got %s)" % x.device)
+    if x.dtype != dtype:
+        raise CsaError("%s must be %s (got %s)" % (what, dtype, x.dtype))
+    if x.device.index != torch.cuda.current_device():
+        raise CsaError("%s is on %s, not on the current device" % (what, x.device))
+    if x.dim() < 2 or x.shape[0] < rows or x.numel() != x.shape[0] * n:
+        raise CsaError("%s must hold %d rows of %d elements (got %s)" % (what, rows, n,
+                                                                     tuple(x.shape)))
+    step = 1
+    for size, stride in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
+        if size != 1 and stride != step:
+            raise CsaError("%s: the elements of a row must be contiguous" % what)
+        step *= size
+    # a single row has no distance to the next: torch may report any
+    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else n
+
+
+def kv_cache(dtype, c, d_hi, rows, hi, scales, block_table):
+    """csa_kv_cache over torch tensors (rows; or E4M3 codes, bf16 dims and scale exponents),
+    which the returned object keeps alive.  The number of pages is the rows' number over
+    PAGE_ENTRIES."""
+    if dtype not in _ELEM:
+        raise CsaError("a cache is F32, BF16 or FP8_E4M3")
+    width = c - d_hi if dtype == CSA_FP8_E4M3 else c
+    if width < 1 or rows.numel() % (width * PAGE_ENTRIES) or rows.numel() == 0:
+        raise CsaError("rows must be whole pages of %d rows of %d elements" % (PAGE_ENTRIES, width))
+    pages = rows.numel() // (width * PAGE_ENTRIES)
+    n = pages * PAGE_ENTRIES
+    if block_table.dim() != 2:
+        raise CsaError("block_table must be [b][max_pages]")
+    if dtype != CSA_FP8_E4M3 and (hi is not None or scales is not None):
+        raise CsaError("hi and scales belong to an FP8 cache")
+    stride = ((c - d_hi) // SCALE_GROUP + 7) // 8 * 8
+    kv = KVCache(dtype=dtype, c=c, d_hi=d_hi, num_pages=pages, max_pages=block_table.shape[1],
+                 rows=_arg(rows, _ELEM[dtype], "rows"), hi=_arg(hi, torch.bfloat16, "hi", n * d_hi),
+                 scales=_arg(scales, torch.uint8, "scales", n * stride),
+                 block_table=_arg(block_table, torch.int32, "block_table"))
+    kv._tensors = (rows, hi, scales, block_table)
+    return kv
+
+
+def alloc_kv_cache(dtype, c, d_hi, num_pages, block_table, device="cuda"):
+    """A paged cache of num_pages pages of zeros for the given block table."""
+    n = num_pages * PAGE_ENTRIES
+    if dtype != CSA_FP8_E4M3:
+        return kv_cache(dtype, c, 0, torch.zeros((n, c), dtype=_ELEM[dtype], device=device), None,
+                        None, block_table)
+    stride = ((c - d_hi) // SCALE_GROUP + 7) // 8 * 8
+    return kv_cache(dtype, c, d_hi, torch.zeros((n, c - d_hi), dtype=torch.uint8, device=device),
+                    torch.zeros((n, d_hi), dtype=torch.bfloat16, device=device) if d_hi else None,
+                    torch.zeros((n, stride), dtype=torch.uint8, device=device), block_table)
+
+
+def _kv(kv, b):
+    """The cache, whose block table must have a row for each of b sequences."""
+    if kv._tensors[3].shape[0] < b:
+        raise CsaError("block_table has %d rows for %d sequences" % (kv._tensors[3].shape[0], b))
+    return ctypes.byref(kv)
+
+
+def csa_cache_write(kv, x_dtype, x, cu_rows, first, b, rows, stream=None):
+    """x: [rows][c], rows possibly strided (a slice of a wider tensor)."""
+    p, stride = _strided(x, _plain(x_dtype), kv.c, rows, "x")
+    _check(lib().csa_cache_write(_kv(kv, b), x_dtype, p, stride,
+                                 _arg(cu_rows, torch.int32, "cu_rows", b + 1),
+                                 _arg(first, torch.int32, "first", b), b, rows, _stream(stream)))
+
+
+def csa_cache_read(kv, idx, count, b, k, out_dtype, out, stream=None):
+    _check(lib().csa_cache_read(_kv(kv, b), _arg(idx, torch.int32, "idx", b * k),
+                                _arg(count, torch.int32, "count", b), b, k, out_dtype,
+                                _arg(out, _plain(out_dtype), "out", b * k * kv.c), _stream(stream)))
+
+
+def csa_window_append(dtype, c, n_w, win, x, cu_rows, first, b, rows, stream=None):
+    p, stride = _strided(x, _plain(dtype), c, rows, "x")
+    _check(lib().csa_window_append(dtype, c, n_w, _arg(win, _plain(dtype), "win", b * n_w * c), p,
+                                   stride, _arg(cu_rows, torch.int32, "cu_rows", b + 1),
+                                   _arg(first, torch.int32, "first", b), b, rows, _stream(stream)))
+
+
+def csa_qk_norm_rope(p, q, q_gain, kv, kv_gain, pos, N, q_out, kv_out, stream=None):
+    """q: [N][H][d] and kv: [N][d], tokens possibly strided; either may be None."""
+    dt = _plain(p.dtype)
+    qp, qs = _strided(q, dt, p.H * p.d, N, "q")
+    kp, ks = _strided(kv, dt, p.d, N, "kv")
+    _check(lib().csa_qk_norm_rope(ctypes.byref(p), qp, qs, _arg(q_gain, torch.float32, "q_gain", p.d),
+                                  kp, ks, _arg(kv_gain, torch.float32, "kv_gain", p.d),
+                                  _arg(pos, torch.int32, "pos", N), N,
+                                  _arg(q_out, dt, "q_out", N * p.H * p.d),
+                                  _arg(kv_out, dt, "kv_out", N * p.d), _stream(stream)))
+
+
+def csa_chunk_attn_workspace_size(p, kv, b, N, L_max):
+    return int(lib().csa_chunk_attn_workspace_size(ctypes.byref(p), ctypes.byref(kv), b, N, L_max))
+
+
+def csa_chunk_attn_launch_count(p, kv, b, N, L_max):
+    return int(lib().csa_chunk_attn_launch_count(ctypes.byref(p), ctypes.byref(kv), b, N, L_max))
+
+
+def csa_chunk_attn(p, kv, q, cu_q, pos0, idx, count, win, new_win, sink, b, N, L_max, out, lse=None,
+                   ws=None, ws_bytes=None, stream=None):
+    dt = _plain(p.dtype)
+    if ws_bytes is None:
+        ws_bytes = ws.numel() * ws.element_size() if isinstance(ws, torch.Tensor) else 0
+    n = N * p.H * p.d
+    _check(lib().csa_chunk_attn(ctypes.byref(p), _kv(kv, b), _arg(q, dt, "q", n),
+                                _arg(cu_q, torch.int32, "cu_q", b + 1),
+                                _arg(pos0, torch.int32, "pos0", b),
+                                _arg(idx, torch.int32, "idx", N * p.k),
+                                _arg(count, torch.int32, "count", N),
+                                _arg(win, dt, "win", b * p.n_w * p.d),
+                                _arg(new_win, dt, "new_win", N * p.d),
+                                _arg(sink, torch.float32, "sink", p.H), b, N, L_max,
+                                _arg(out, dt, "out", n), _arg(lse, torch.float32, "lse", N * p.H),
+                                _ptr(ws), ws_bytes, _stream(stream)))

@@ -150,6 +150,54 @@ int out_proj_launch_count(int T, int H, int d, int g, int d_g);
 csa_status launch_out_proj(const void* o, const void* W, int T, int H, int d, int g, int d_g,
                            void* y, void* ws, size_t ws_bytes, cudaStream_t st, bool pdl);
 
+// Chunks of new tokens over a paged latent cache (see csa.h).
+constexpr int kScaleGroup = 64;   // dims sharing one scale of an FP8 row
+constexpr int kScaleExpMin = -110, kScaleExpMax = 119;
+
+// Bytes of one row's scales: one exponent per group, padded to whole 8-byte words.
+__host__ __device__ inline int kv_scale_stride(int c, int d_hi) {
+  return ((c - d_hi) / kScaleGroup + 7) / 8 * 8;
+}
+
+struct NormRopeArgs {
+  const void *q, *kv; void *q_out, *kv_out;
+  long long q_stride, kv_stride;   // elements between tokens
+  const float *q_gain, *kv_gain;
+  const int32_t* pos;
+  int H, d, d_rope, N, norm;
+  float eps;
+  double inv_freq[kMaxRopePairs];   // theta^(-2j/d_rope) in float64
+};
+
+struct RowsArgs {   // ragged rows: row cu[s] + j of sequence s is its item first[s] + j
+  const void* x; long long x_stride;
+  const int32_t *cu, *first;
+  int b, rows;
+};
+
+struct ChunkArgs {
+  const void* q; const int32_t *cu_q, *pos0, *idx, *count;
+  const void *win, *new_win; const float* sink;
+  void* out; float* lse;
+  int b, N, H, d, n_w, m, k, L_max, d_rope_out;
+  float scale;
+  double theta;
+};
+
+csa_status launch_norm_rope(NormRopeArgs& a, int dtype, double theta, cudaStream_t st);
+csa_status launch_cache_write(const csa_kv_cache& kv, int x_dtype, const RowsArgs& a, cudaStream_t st);
+csa_status launch_cache_read(const csa_kv_cache& kv, const int32_t* idx, const int32_t* count, int b,
+                             int k, int out_dtype, void* out, cudaStream_t st);
+csa_status launch_window_append(int dtype, int c, int n_w, void* win, const RowsArgs& a,
+                                cudaStream_t st);
+csa_status launch_chunk_attn_simt(const ChunkArgs& a, const csa_kv_cache& kv, int dtype,
+                                  cudaStream_t st);
+bool chunk_tc_supported(int H, int d, int dtype, int d_rope_out, const csa_kv_cache& kv);
+size_t chunk_tc_workspace_bytes(int n_w, int m, int k, int N, int L_max);
+int chunk_tc_launch_count(int n_w, int m, int k, int N, int L_max);
+csa_status launch_chunk_attn_tc(const ChunkArgs& a, const csa_kv_cache& kv, void* ws,
+                                size_t ws_bytes, cudaStream_t st);
+
 // Small helpers.
 csa_status launch_fill_i32(int32_t* p, int count, int value, cudaStream_t st);
 csa_status launch_iota_positions(int32_t* p, int b, int n, cudaStream_t st);

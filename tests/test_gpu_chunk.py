@@ -1,0 +1,443 @@
+"""The calls that serve a chunk of new tokens over a paged cache, against the float64 oracle.
+
+Tolerances, derived before the first run:
+ * Cache writes and reads are exact: a code is one rounding of a value scaled by a power of
+   two, and what it stands for is a bf16 value.
+ * Norm and rotation: a bf16 result is off by at most half a step (2^-8 of its value); the
+   float32 arithmetic before it by (d/32 + 16) 2^-24 (a lane's d/32 terms of the sum of
+   squares, five shuffles, root, division, two products) of the value, and by 2^-21 of the
+   pair's |x0| + |x1| for a rotated one (the reduced angle, up to pi, is rounded to float32:
+   2^-23; its sine and cosine to 2^-23 again; two products and a sum).
+ * Attention: with l the logits and A = sum_r w_r |row_r| the weighted magnitudes (both from
+   the oracle), rounding the logits by dl moves the output by at most 2 dl A and the lse by dl.
+   dl <= scale |q|.|row| 2^-14 covers 512 float32 accumulations with an error of a whole
+   last place each (2^-23); small head dims lie far below.  The accumulation over R rows adds
+   R 2^-23 A, the exponentials 2^-21 A.  In bf16 each weight is rounded (2^-8) and so is the
+   result (2^-8): 2^-8 (A + |o|).  The inverse rotation mixes a pair: its A is the pair's sum,
+   and the angle adds 2^-21 of it.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from long_context_sparse_05_b200 import _lib as L
+from oracle import chunk, csa
+
+from helpers import f64
+
+pytestmark = pytest.mark.gpu
+
+PE = L.PAGE_ENTRIES
+THETA, EPS = 10000.0, 1e-6
+TDT = {L.CSA_F32: torch.float32, L.CSA_BF16: torch.bfloat16}
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def starts(lens):
+    return [0] + np.cumsum(lens).tolist()
+
+
+def randn(seed, shape, dtype=torch.float32):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda").to(dtype)
+
+
+def table(entries, seed=0, extra=1, max_pages=None):
+    """(pages, block table) of sequences with the given entries, pages shuffled."""
+    need = [-(-e // PE) for e in entries]
+    total = sum(need) + extra
+    perm = np.random.default_rng(seed).permutation(total)
+    bt = np.full((len(entries), max_pages or max(1, max(need))), -1, dtype=np.int32)
+    at = 0
+    for s, n in enumerate(need):
+        bt[s, :n] = perm[at:at + n]
+        at += n
+    return total, bt
+
+
+def place(bt, s, e):
+    return int(bt[s, e // PE]) * PE + e % PE
+
+
+# ----------------------------------------------------------------------------- norm, rotation
+
+@pytest.mark.parametrize("dtype,N,H,d,d_rope,gain,strided,norm", [
+    (L.CSA_BF16, 1, 64, 512, 64, True, False, 1),
+    (L.CSA_BF16, 5, 64, 512, 64, False, True, 1),
+    (L.CSA_BF16, 331, 64, 512, 64, True, True, 1),     # several rows per warp, tokens straddle warps
+    (L.CSA_BF16, 17, 64, 128, 64, False, False, 0),    # index queries: rotation alone
+    (L.CSA_F32, 33, 4, 64, 16, True, False, 1),
+    (L.CSA_F32, 9, 3, 40, 6, True, True, 1),           # rotary dims starting inside a chunk of 8
+    (L.CSA_F32, 2, 1, 8, 8, False, False, 1),
+    (L.CSA_F32, 3, 2, 2048, 128, True, False, 1),
+    (L.CSA_BF16, 4, 2, 1000, 0, True, False, 1),
+])
+def test_norm_rope(dtype, N, H, d, d_rope, gain, strided, norm):
+    dt = TDT[dtype]
+    if strided:
+        buf = randn(1, (N, (H + 1) * d + 16), dt)
+        q, kv = buf[:, : H * d].view(N, H, d), buf[:, H * d:(H + 1) * d]
+    else:
+        q, kv = randn(1, (N, H, d), dt), randn(2, (N, d), dt)
+    qg = (1 + 0.2 * randn(3, (d,))) if gain else None
+    kg = (1 + 0.2 * randn(4, (d,))) if gain else None
+    pos = [(i * 7919 + 3) % (1 << 20) for i in range(N)]
+    qo, ko = torch.empty((N, H, d), dtype=dt, device="cuda"), torch.empty((N, d), dtype=dt, device="cuda")
+    p = L.NormRopeParams(H=H, d=d, d_rope=d_rope, rope_theta=THETA, eps=EPS, apply_norm=norm, dtype=dtype)
+    L.csa_qk_norm_rope(p, q, qg, kv, kg, i32(pos), N, qo, ko)
+    rows = sorted(set([0, N - 1, N // 2] + list(range(min(N, 6)))))
+    for out, x, g in ((qo, q, qg), (ko[:, None], kv[:, None], kg)):
+        for n in rows:
+            xr = f64(x[n])
+            y0 = chunk.norm_rope(xr, None if g is None else f64(g), np.zeros(len(xr)), 0, THETA, EPS, bool(norm))
+            ref = csa.rope_partial(y0, np.full(len(xr), float(pos[n])), d_rope, THETA)
+            tol = (d / 32 + 16) * 2.0 ** -24 * np.abs(ref)
+            if d_rope:
+                pair = np.abs(y0[:, d - d_rope:]).reshape(len(xr), -1, 2).sum(-1)
+                tol[:, d - d_rope:] += np.repeat(pair, 2, axis=1) * ((d / 32 + 16) * 2.0 ** -24 + 2.0 ** -21)
+            if dtype == L.CSA_BF16:
+                tol += 2.0 ** -8 * np.abs(ref)
+            err = np.abs(f64(out[n]) - ref)
+            assert np.all(err <= tol + 1e-37), (n, float(np.max(err / (tol + 1e-37))))
+
+
+def test_norm_rope_one_side_and_in_place():
+    N, H, d = 6, 64, 512
+    q, kv = randn(5, (N, H, d), torch.bfloat16), randn(6, (N, d), torch.bfloat16)
+    pos = i32([5] * N)
+    p = L.NormRopeParams(H=H, d=d, d_rope=64, rope_theta=THETA, eps=EPS, apply_norm=1, dtype=L.CSA_BF16)
+    qo, ko = torch.empty_like(q), torch.empty_like(kv)
+    L.csa_qk_norm_rope(p, q, None, kv, None, pos, N, qo, ko)
+    q1, k1 = torch.empty_like(q), torch.empty_like(kv)
+    L.csa_qk_norm_rope(p, q, None, None, None, pos, N, q1, None)
+    L.csa_qk_norm_rope(p, None, None, kv, None, pos, N, None, k1)
+    assert torch.equal(q1, qo) and torch.equal(k1, ko)
+    L.csa_qk_norm_rope(p, q, None, kv, None, pos, N, q, kv)
+    assert torch.equal(q, qo) and torch.equal(kv, ko)
+
+
+# ----------------------------------------------------------------------------- the cache
+
+def cache_of(fmt, c, d_hi, total, bt, fill=None):
+    kv = L.alloc_kv_cache(fmt, c, d_hi, total, torch.from_numpy(bt).cuda())
+    if fill is not None:
+        for t in kv._tensors[:3]:
+            if t is not None:
+                t.view(torch.uint8).fill_(fill)
+    return kv
+
+
+@pytest.mark.parametrize("fmt,x_dtype,c,d_hi,lens,first", [
+    (L.CSA_FP8_E4M3, L.CSA_BF16, 512, 64, [1] * 5, [0, 255, 256, 700, 511]),
+    (L.CSA_FP8_E4M3, L.CSA_BF16, 512, 64, [300, 0, 1, 517, 0], [250, 3, 255, 1, 0]),
+    (L.CSA_FP8_E4M3, L.CSA_F32, 512, 64, [33, 2], [0, 254]),
+    (L.CSA_FP8_E4M3, L.CSA_BF16, 64, 0, [7], [3]),
+    (L.CSA_FP8_E4M3, L.CSA_F32, 1104, 16, [5, 3], [254, 0]),      # more than one pass, odd widths
+    (L.CSA_FP8_E4M3, L.CSA_BF16, 512, 64, [39000, 77], [0, 9]),   # several rows per warp
+    (L.CSA_BF16, L.CSA_BF16, 512, 0, [3, 270], [255, 0]),
+    (L.CSA_BF16, L.CSA_F32, 40, 0, [3, 1], [0, 2]),
+    (L.CSA_F32, L.CSA_F32, 8, 0, [2, 300], [1, 0]),
+    (L.CSA_F32, L.CSA_BF16, 64, 0, [4], [254]),
+])
+def test_cache_write_and_read(fmt, x_dtype, c, d_hi, lens, first):
+    b, n = len(lens), sum(lens)
+    total, bt = table([f + l for f, l in zip(first, lens)], seed=3, extra=2)
+    kv = cache_of(fmt, c, d_hi, total, bt, fill=0xA5)
+    before = [None if t is None else t.clone() for t in kv._tensors[:3]]
+    x = randn(7, (n + 3, c), TDT[x_dtype])
+    x[:, ::5] *= 30.0                                  # groups of very different sizes
+    x[0, : min(c, 64)] = 0.0
+    if fmt == L.CSA_FP8_E4M3 and n > 2:
+        x[1, 0], x[1, 1] = 448.0, -448.0 * 2.0 ** -30
+        x[2, 0] = 1.0e-42 if x_dtype == L.CSA_F32 else 2.0 ** -130
+    cu = starts(lens)
+    # rows counted beyond the last sequence's are not written
+    L.csa_cache_write(kv, x_dtype, x, i32(cu), i32(first), b, n + 3)
+    torch.cuda.synchronize()
+    xs = f64(x)
+    arrs = [None if t is None else t.cpu() for t in kv._tensors[:3]]
+    touched = set()
+    rng = np.random.default_rng(0)
+    for s in range(b):
+        js = range(lens[s]) if lens[s] <= 600 else sorted(set([0, 1, lens[s] - 1]) | set(rng.integers(0, lens[s], 60).tolist()))
+        touched |= {place(bt, s, first[s] + j) for j in range(lens[s])}
+        for j in js:
+            at, row = place(bt, s, first[s] + j), xs[cu[s] + j]
+            if fmt == L.CSA_FP8_E4M3:
+                codes, hi, exps = chunk.quant_row(row, d_hi)
+                assert np.array_equal(arrs[0][at].numpy(), codes), (s, j)
+                assert np.array_equal(arrs[2][at].numpy()[: len(exps)], exps), (s, j)
+                if d_hi:
+                    assert np.array_equal(f64(arrs[1][at]), hi)
+            else:
+                assert torch.equal(arrs[0][at].cuda(), x[cu[s] + j].to(TDT[fmt]))
+    # every other row as it was, and the spare scale bytes too
+    rest = torch.ones(total * PE, dtype=torch.bool)
+    rest[torch.tensor(sorted(touched), dtype=torch.long)] = False
+    for t, t0 in zip(arrs, before):
+        if t is not None:
+            assert torch.equal(t.view(torch.uint8)[rest], t0.cpu().view(torch.uint8)[rest])
+    if fmt == L.CSA_FP8_E4M3:
+        ng = (c - d_hi) // 64
+        assert torch.all(arrs[2][:, ng:] == 0xA5)
+    # read back: selected entries in any order, a repeated one, ones outside, and whole ranges
+    kmax = max(max(first[s] + lens[s] for s in range(b)), 4) + 2
+    k = min(kmax, 300)
+    idx = rng.integers(-2, kmax, (b, k)).astype(np.int32)
+    idx[0, :4] = [first[0], first[0], 2 ** 31 - 1, -2 ** 31]
+    count = np.array([k - (s % 3) for s in range(b)], dtype=np.int32)
+    for out_dtype in (L.CSA_F32, L.CSA_BF16):
+        for sel in (idx, None):
+            out = torch.full((b, k, c), float("nan"), dtype=TDT[out_dtype], device="cuda")
+            L.csa_cache_read(kv, None if sel is None else i32(sel.tolist()), i32(count.tolist()), b, k,
+                             out_dtype, out)
+            for s in range(b):
+                for j in list(range(6)) + [k // 2, k - 2, k - 1]:
+                    e = int(sel[s, j]) if sel is not None else j
+                    held = 0 <= e < bt.shape[1] * PE and j < count[s] and bt[s, e // PE] >= 0
+                    if not held:
+                        assert torch.all(out[s, j] == 0), (s, j, e)
+                        continue
+                    at = place(bt, s, e)
+                    if at not in touched:
+                        continue               # filler bytes: not numbers to compare
+                    if fmt == L.CSA_FP8_E4M3:
+                        hi = f64(arrs[1][at]) if d_hi else np.zeros(0)
+                        ref = chunk.dequant_row(arrs[0][at].numpy(), hi, arrs[2][at].numpy()[: (c - d_hi) // 64])
+                        assert np.array_equal(f64(out[s, j]), ref), (s, j, e)
+                    else:
+                        assert torch.equal(out[s, j], arrs[0][at].cuda().to(TDT[out_dtype]))
+
+
+def test_cache_write_strided_rows_and_specials():
+    c, d_hi = 512, 64
+    total, bt = table([20], seed=1)
+    wide = randn(8, (20, 2 * c + 8), torch.bfloat16)
+    wide[0, c], wide[0, c + 1] = float("nan"), 3.0
+    wide[1, c + 64], wide[1, c + 65] = float("inf"), -float("inf")
+    wide[2, c:c + 64] = float("nan")
+    x = wide[:, c:2 * c]
+    kv = cache_of(L.CSA_FP8_E4M3, c, d_hi, total, bt)
+    L.csa_cache_write(kv, L.CSA_BF16, x, i32([0, 20]), i32([0]), 1, 20)
+    out = torch.empty((1, 20, c), dtype=torch.bfloat16, device="cuda")
+    L.csa_cache_read(kv, None, None, 1, 20, L.CSA_BF16, out)
+    for j in range(20):
+        codes, hi, exps = chunk.quant_row(f64(x[j]), d_hi)
+        assert np.array_equal(kv._tensors[0][place(bt, 0, j)].cpu().numpy(), codes), j
+        np.testing.assert_array_equal(f64(out[0, j]), chunk.dequant_row(codes, hi, exps))
+
+
+def test_cache_skips_pages_and_entries_outside():
+    """A table entry outside the pool, entries past the table and before 0: nothing is written
+    there, nothing is read."""
+    c = 64
+    bt = np.array([[0, 7, 1], [-1, 2, -5]], dtype=np.int32)     # 7 and the negatives: no page
+    kv = cache_of(L.CSA_BF16, c, 0, 4, bt)
+    x = torch.ones((1600, c), dtype=torch.bfloat16, device="cuda")
+    L.csa_cache_write(kv, L.CSA_BF16, x, i32([0, 800, 1600]), i32([0, -20]), 2, 1600)
+    rows = kv._tensors[0].view(4, PE, c)
+    assert torch.all(rows[0] == 1) and torch.all(rows[1] == 1) and torch.all(rows[2] == 1)
+    assert torch.all(rows[3] == 0)
+    out = torch.full((2, 900, c), 9.0, dtype=torch.bfloat16, device="cuda")
+    L.csa_cache_read(kv, None, None, 2, 900, L.CSA_BF16, out)
+    ok = torch.zeros((2, 900), dtype=torch.bool)
+    ok[0, :256] = ok[0, 512:768] = ok[1, 256:512] = True
+    assert torch.equal((out[:, :, 0] == 1).cpu(), ok) and torch.all(out[~ok.cuda()] == 0)
+
+
+@pytest.mark.parametrize("dtype,c,n_w", [(L.CSA_BF16, 512, 128), (L.CSA_F32, 64, 16), (L.CSA_BF16, 8, 1)])
+def test_window_append(dtype, c, n_w):
+    """The rings after a chunk are what appending token by token leaves, whatever its length."""
+    lens, first = [1, 3 * n_w + 5, 0, n_w, 7], [5, 1000, 3, 0, n_w - 1]
+    b, n = len(lens), sum(lens)
+    win = randn(1, (b, n_w, c), TDT[dtype])
+    x = randn(2, (n + 2, c + 8), TDT[dtype])[:, :c]
+    want = win.clone()
+    cu = starts(lens)
+    for s in range(b):
+        for j in range(lens[s]):
+            want[s, (first[s] + j) % n_w] = x[cu[s] + j]
+    L.csa_window_append(dtype, c, n_w, win, x, i32(cu), i32(first), b, n + 2)
+    assert torch.equal(win, want)
+
+
+# ----------------------------------------------------------------------------- attention
+
+class Case:
+    """A ragged chunk over a paged cache with everything random, and its oracle."""
+
+    def __init__(self, lens, ctx, H, d, m, k, n_w, dtype, fmt, d_hi=0, d_rope_out=0, seed=0,
+                 sink=None, pad=2, counts=None, hole=False, qscale=1.0):
+        self.__dict__.update(lens=lens, ctx=ctx, H=H, d=d, m=m, k=k, n_w=n_w, dtype=dtype, fmt=fmt,
+                             d_hi=d_hi)
+        b, n = len(lens), sum(lens)
+        dt = TDT[dtype]
+        self.b, self.N, self.cu = b, n + pad, starts(lens)
+        ents = [(p + l) // m for p, l in zip(ctx, lens)]
+        total, self.bt = table(ents, seed=seed)
+        if hole and self.bt.shape[1] > 1:
+            self.bt[0, 0] = total + 3                # a page outside the pool
+        self.kv = cache_of(fmt, d, d_hi, total, self.bt)
+        rows = randn(seed + 1, (total * PE, d))
+        if fmt == L.CSA_FP8_E4M3:
+            flat = L.alloc_kv_cache(fmt, d, d_hi, total, i32([list(range(total))]))
+            flat.rows, flat.hi, flat.scales = self.kv.rows, self.kv.hi, self.kv.scales
+            L.csa_cache_write(flat, L.CSA_F32, rows, i32([0, total * PE]), i32([0]), 1, total * PE)
+        else:
+            self.kv._tensors[0].copy_(rows)
+        self.q = (randn(seed + 2, (self.N, H, d)) * qscale).to(dt)
+        self.win = randn(seed + 3, (b, max(n_w, 1), d), dt)
+        self.new_win = randn(seed + 4, (self.N, d), dt)
+        self.sink = randn(seed + 5, (H,)) if sink is None else torch.full((H,), sink, device="cuda")
+        self.idx = self.count = None
+        if k:
+            rng = np.random.default_rng(seed)
+            idx, count = np.full((self.N, k), -1, dtype=np.int32), np.zeros(self.N, dtype=np.int32)
+            for s in range(b):
+                for i in range(lens[s]):
+                    E = (ctx[s] + i + 1) // m
+                    r = self.cu[s] + i
+                    c = min(E, k) if counts is None else min(counts, k)
+                    pick = np.sort(rng.choice(E, min(E, c), replace=False)) if E else np.zeros(0, int)
+                    idx[r, :len(pick)] = pick
+                    count[r] = c
+            self.idx, self.count = i32(idx.tolist()), i32(count.tolist())
+        self.L_max = max(p + l for p, l in zip(ctx, lens))
+        self.p = L.AttnParams(H=H, d=d, n_w=n_w, scale=1.0 / math.sqrt(d), m=m, k=k, dtype=dtype,
+                              d_rope_out=d_rope_out, rope_theta=THETA)
+        self.out = torch.full((self.N, H, d), 7.0, dtype=dt, device="cuda")
+        self.lse = torch.full((self.N, H), 7.0, device="cuda")
+        nb = L.csa_chunk_attn_workspace_size(self.p, self.kv, b, self.N, self.L_max)
+        self.ws = torch.full((max(nb, 16),), 0xFF, dtype=torch.uint8, device="cuda")
+
+    def run(self, stream=None):
+        L.csa_chunk_attn(self.p, self.kv, self.q, i32(self.cu), i32(self.ctx), self.idx, self.count,
+                         self.win if self.n_w else None, self.new_win if self.n_w else None, self.sink,
+                         self.b, self.N, self.L_max, self.out, self.lse, self.ws, stream=stream)
+        torch.cuda.synchronize()
+        assert L.csa_device_error() == 0
+        return self
+
+    def entry(self, s, e):
+        pg = int(self.bt[s, e // PE])
+        if not 0 <= pg < self.kv.num_pages:
+            return None
+        at = pg * PE + e % PE
+        if self.fmt != L.CSA_FP8_E4M3:
+            return self.rows64[at]
+        return self.rows64[at]
+
+    def values(self):
+        """The pool's rows as float64."""
+        a = self.kv._tensors
+        if self.fmt != L.CSA_FP8_E4M3:
+            return f64(a[0])
+        out = torch.empty((1, self.kv.num_pages * PE, self.d), dtype=torch.float32, device="cuda")
+        flat = L.alloc_kv_cache(self.fmt, self.d, self.d_hi, 1, i32([list(range(self.kv.num_pages))]))
+        flat.num_pages, flat.rows, flat.hi, flat.scales = (self.kv.num_pages, self.kv.rows,
+                                                           self.kv.hi, self.kv.scales)
+        L.csa_cache_read(flat, None, None, 1, self.kv.num_pages * PE, L.CSA_F32, out)
+        return f64(out[0])
+
+    def check(self, tokens=None):
+        self.rows64 = self.values()
+        q, win, nw, sink = f64(self.q), f64(self.win), f64(self.new_win), f64(self.sink)
+        out, lse = f64(self.out), f64(self.lse)
+        d, r_out = self.d, self.p.d_rope_out
+        bf = self.dtype == L.CSA_BF16
+        for s in range(self.b):
+            picks = range(self.lens[s]) if tokens is None else sorted(
+                {0, self.lens[s] - 1} | set(np.linspace(0, self.lens[s] - 1, tokens).astype(int))) if self.lens[s] else []
+            for i in picks:
+                row = self.cu[s] + i
+                sel = None
+                if self.k:
+                    sel = self.idx[row].cpu().numpy()[: int(self.count[row])]
+                t, rows = chunk.chunk_rows(s, i, self.entry, sel, self.ctx[s], self.cu[s], self.m,
+                                           self.bt.shape[1] * PE, win, nw, self.n_w)
+                o, l, A = chunk.attend(q[row], rows, sink, self.p.scale)
+                R = np.asarray(rows) if rows else np.zeros((1, d))
+                dl = self.p.scale * (np.abs(q[row]) @ np.abs(R).T).max(axis=1) * 2.0 ** -14
+                n = len(rows)
+                tol = A * (2 * dl[:, None] + n * 2.0 ** -23 + 2.0 ** -21)
+                if bf:
+                    tol += 2.0 ** -8 * A
+                if r_out:
+                    o = csa.inverse_rope(o, t, r_out, THETA)
+                    pair = tol[:, d - r_out:].reshape(self.H, -1, 2).sum(-1)
+                    mag = A[:, d - r_out:].reshape(self.H, -1, 2).sum(-1) * 2.0 ** -21
+                    tol[:, d - r_out:] = np.repeat(pair + mag, 2, axis=1)
+                if bf:
+                    tol += 2.0 ** -8 * np.abs(o)
+                err = np.abs(out[row] - o)
+                assert np.all(err <= tol + 1e-30), (s, i, t, float(np.max(err / (tol + 1e-30))))
+                fin = np.isfinite(l)
+                assert np.array_equal(lse[row][~fin], l[~fin])
+                ltol = dl + n * 2.0 ** -23 + 2.0 ** -20 + 2.0 ** -22 * np.abs(np.where(fin, l, 0))
+                assert np.all(np.abs(lse[row] - np.where(fin, l, 0))[fin] <= ltol[fin]), (s, i)
+        # rows behind the last sequence stay as they were
+        assert torch.all(self.out[self.cu[-1]:] == 7.0) and torch.all(self.lse[self.cu[-1]:] == 7.0)
+
+
+SMALL = dict(H=4, d=64, m=4, n_w=16, dtype=L.CSA_F32, fmt=L.CSA_F32)
+TC = dict(H=64, d=512, n_w=128, dtype=L.CSA_BF16)
+
+
+@pytest.mark.parametrize("k", [0, 16])
+@pytest.mark.parametrize("over", [
+    dict(), dict(H=3, d=40, n_w=5), dict(H=1, d=8, n_w=0), dict(dtype=L.CSA_BF16, fmt=L.CSA_BF16, d_rope_out=16),
+    dict(fmt=L.CSA_FP8_E4M3, d=128, d_hi=64, d_rope_out=64),
+    dict(dtype=L.CSA_BF16, fmt=L.CSA_FP8_E4M3, d=80, d_hi=16, m=128, n_w=128),
+])
+def test_chunk_attn_any_shape(k, over):
+    cfg = dict(SMALL, **over)
+    Case([5, 0, 1, 33], [0, 9, 1027, 300], k=k, seed=11, **cfg).run().check()
+
+
+@pytest.mark.parametrize("fmt,d_hi", [(L.CSA_BF16, 0), (L.CSA_FP8_E4M3, 64)])
+@pytest.mark.parametrize("lens,ctx,m,k,d_rope_out", [
+    ([1], [0], 4, 0, 0),                                  # the very first token: a window of one row
+    ([1, 1, 1], [511, 5000, 2], 4, 512, 64),              # single tokens, selections cut by E(t) and k
+    ([1, 1], [128 * 700 + 17, 128 * 300 - 1], 128, 0, 64),  # long dense rows, split over CTAs
+    ([7, 0, 130, 1], [1000, 4, 0, 40000], 4, 512, 64),    # ragged, an empty sequence, a fresh prompt
+    ([40, 3], [128 * 256 - 20, 128 * 40], 128, 0, 0),     # visible entries cross a page inside the chunk
+    ([200, 101], [3000, 0], 4, 37, 64),                   # a selection of an odd length
+])
+def test_chunk_attn_tensor_core(fmt, d_hi, lens, ctx, m, k, d_rope_out):
+    Case(lens, ctx, m=m, k=k, fmt=fmt, d_hi=d_hi, d_rope_out=d_rope_out, seed=21, **TC).run().check(tokens=6)
+
+
+@pytest.mark.parametrize("fmt,d_hi", [(L.CSA_BF16, 0), (L.CSA_FP8_E4M3, 64)])
+@pytest.mark.parametrize("cfg", [
+    dict(n_w=0, k=64, counts=0),                    # no row at all: zeros, the sink as lse
+    dict(n_w=0, k=64, counts=0, sink=-math.inf),    # nor a sink: lse -inf
+    dict(n_w=0, k=0),                               # E(t) = 0 for the first tokens
+    dict(n_w=1, k=64),
+    dict(n_w=300, k=64),                            # a window of more than two tiles
+    dict(n_w=128, k=64, sink=-math.inf),
+    dict(n_w=128, k=64, sink=200.0),                # a sink far above every logit
+    dict(n_w=128, k=64, sink=-200.0),
+    dict(n_w=128, k=700, hole=True),                # selected entries on a page outside the pool
+    dict(n_w=0, k=64, hole=True, ctx=[900, 40]),    # every selected entry outside: weights of nothing
+    dict(n_w=128, k=300, counts=300, ctx=[400, 0]),  # count beyond the valid entries: -1 padding inside
+    dict(n_w=128, k=512, qscale=30.0),              # one row takes nearly all the weight
+])
+def test_chunk_attn_masks_and_edges(fmt, d_hi, cfg):
+    c = dict(TC, lens=[5, 3], ctx=[2500, 1], m=4, seed=31, fmt=fmt, d_hi=d_hi)
+    c.update(cfg)
+    Case(**c).run().check()
+
+
+def test_chunk_attn_small_shape_edges():
+    for cfg in (dict(n_w=0, k=16, counts=0), dict(n_w=0, k=16, counts=0, sink=-math.inf),
+                dict(n_w=16, k=0, sink=-math.inf), dict(n_w=0, k=0), dict(n_w=3, k=16, hole=True),
+                dict(n_w=16, k=16, sink=90.0), dict(n_w=0, k=8, hole=True)):
+        c = dict(SMALL, lens=[5, 3], ctx=[2500, 1], seed=41)
+        c.update(cfg)
+        Case(**c).run().check()
