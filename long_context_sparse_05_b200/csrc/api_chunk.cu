@@ -132,8 +132,10 @@ csa_status csa_chunk_attn(const csa_attn_params* p, const csa_kv_cache* kv, cons
   a.new_win = new_win; a.sink = sink; a.out = out; a.lse = lse; a.b = b; a.N = N; a.H = p->H;
   a.d = p->d; a.n_w = p->n_w; a.m = p->m; a.k = p->k; a.L_max = L_max;
   a.d_rope_out = p->d_rope_out; a.scale = p->scale; a.theta = p->rope_theta;
-  if (chunk_tc_supported(p->H, p->d, p->dtype, p->d_rope_out, *kv))
-    return launch_chunk_attn_tc(a, *kv, ws, ws_bytes, stream);
+  if (chunk_tc_supported(p->H, p->d, p->dtype, p->d_rope_out, *kv)) {
+    const csa_status st = launch_chunk_attn_tc(a, *kv, ws, ws_bytes, stream);
+    if (st != CSA_ERR_UNSUPPORTED) return st;
+  }
   return launch_chunk_attn_simt(a, *kv, p->dtype, stream);
 }
 

@@ -1,7 +1,828 @@
-#include "kernels.h"
+// Attention of a chunk of new tokens over a paged cache on the tcgen05 tensor cores
+// (sm_100a): 64 heads of 512 dims, bf16 queries, bf16 or FP8 pages.
+//
+// Method: "DeepSeek Technical Reports", sections DSA and CSA; "DeepSeek V4 结构速览",
+// sections "CSA（c4a 路线）" and "HCA（c128a 路线）" (selected or all visible entries, then the
+// raw sliding window; K = V; a sink per head).
+//
+// A token's rows are cut into tiles of 128: entry tiles first, then window tiles, so that a
+// tile's rows have one format.  Per tile, with rows on the MMA's M and heads on N:
+//   S^T[r, h]  = KV[r] . q[h]            (M = 128 rows, N = 64 heads, K = 512)
+//   O^T[d, h] += V^T[d, r] P^T[r, h]     (M = 4 x 128 dims, N = 64, K = 128 rows)
+// both from the same swizzled shared-memory tile (eight column blocks of 64 dims), so a row
+// is read once.  P^T goes through shared memory; S^T and O^T live in TMEM.
+//
+// What bounds it: the two products of a tile take ~3,200 cycles (at N = 64 an MMA reads 6 KB
+// of operands, 48 cycles at 128 bytes a cycle, for 32 cycles of math), and one tile of
+// shared memory (128 KB, beside 64 KB of queries) leaves no room for a second.  So the next
+// tile waits in registers: as soon as a tile has been stored, every softmax thread issues the
+// loads of its share of the next one (three of the four 128-dim pairs in bf16, all of it in
+// FP8), which travel under this tile's softmax and PV; each pair is stored the moment the PV
+// has read its predecessor, and its S^T MMAs start on it.  FP8 rows become bf16 on the way
+// to shared memory (code times a power of two: exact).
+//
+// The softmax keeps the maximum lazily (raised only when a tile exceeds it by 2^8, which
+// rescales O^T in TMEM) and each thread's sums of its 32 heads in registers over the tiles of
+// an item: the reduction over the rows runs once per item, so an ordinary tile needs one
+// barrier (the OR of "some logit exceeds the maximum") before its probabilities.
+//
+// Work item = (token, split of its tiles); CTAs walk the items with stride gridDim.x.  Few
+// tokens are split over several CTAs (fp32 partials, combined by chunk_merge_kernel), many
+// are not.  The rows' addresses come from a chain of loads (selection -> block table ->
+// row), run two tiles ahead of their use.
+#include "chunk_common.cuh"
+#include "tc_common.cuh"
+#include "xpose.cuh"
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
 namespace csa {
-bool chunk_tc_supported(int, int, int, int, const csa_kv_cache&) { return false; }
-size_t chunk_tc_workspace_bytes(int, int, int, int, int) { return 0; }
-int chunk_tc_launch_count(int, int, int, int, int) { return 1; }
-csa_status launch_chunk_attn_tc(const ChunkArgs&, const csa_kv_cache&, void*, size_t, cudaStream_t) { return CSA_ERR_UNSUPPORTED; }
+
+namespace {
+
+constexpr int kH = 64;            // heads
+constexpr int kD = 512;           // head dim = latent dim
+constexpr int kHi = 64;           // bf16 dims of an FP8 row
+constexpr int kNc = kD - kHi;     // its codes
+constexpr int kRows = 128;        // rows per tile
+constexpr int kKVBlk = kRows * 128;   // bytes of one column block of the tile
+constexpr int kQBlk = kH * 128;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescale = 8.0f;      // log2 units
+constexpr int kSW = 8;                // softmax / gather warps: two per TMEM lane quarter
+constexpr int kST = 32 * kSW;
+constexpr int kThr = kST + 32;        // plus the MMA warp: the threads of the tile barriers
+// The CTA is launched with three whole warpgroups (the MMA warp and three that idle make the
+// third) of 168 registers a thread, the most that fits; the third hands most of its share to
+// the other two, which hold a tile in registers: 2 x 216 + 72 = 3 x 168.
+constexpr int kLaunch = 384;
+constexpr int kRegsSoftmax = 216, kRegsMma = 72;
+static_assert(2 * kRegsSoftmax + kRegsMma <= 3 * 168, "setmaxnreg shares");
+constexpr uint32_t kHintNs = 64;
+constexpr int kSeqCache = 1024;       // sequences whose boundaries are kept in shared memory
+constexpr int kMaxSplit = 32;
+constexpr int kNewTag = 1 << 30;      // window rows: new_win's row + kNewTag, or the rings' row
+
+struct ChunkTc {
+  const __nv_bfloat16 *q, *win, *new_win;
+  const int32_t *cu_q, *pos0, *idx, *count;
+  const float* sink;
+  __nv_bfloat16* out;
+  float* lse;
+  float *part_o, *part_m, *part_l;   // per item [512][64], [64], [64]
+  int* err;
+  csa_kv_cache kv;
+  int b, N, n_w, m, k, nsplit, items, d_rope_out;
+  float scale_log2;
+  double inv_freq[kMaxOutRopePairs];
+};
+
+struct Item {
+  int tok, seq, i0, p0, t, nsel, ne, w0, tb, te;
+  bool live;
+};
+
+// Item `item` (whole warp).  cu / pos0 point to shared or global memory.
+__device__ __forceinline__ Item get_item(const ChunkTc& p, const int32_t* cu, const int32_t* pos0,
+                                         int item, int lane) {
+  Item I;
+  I.tok = item / p.nsplit;
+  const int split = item - I.tok * p.nsplit;
+  I.seq = find_seq(cu, p.b, I.tok, lane);
+  I.live = I.seq < p.b && I.tok >= cu[0];
+  if (!I.live) {
+    I.i0 = I.p0 = I.t = I.nsel = I.ne = I.w0 = I.tb = I.te = 0;
+    return I;
+  }
+  I.i0 = cu[I.seq];
+  I.p0 = pos0[I.seq];
+  I.t = I.p0 + (I.tok - I.i0);
+  int ns = 0, nwin = 0;
+  I.w0 = 0;
+  if (I.t >= 0) {
+    ns = p.idx ? min(p.count[I.tok], p.k) : min((I.t + 1) / p.m, p.kv.max_pages * kPageEntries);
+    I.w0 = max(0, I.t - p.n_w + 1);
+    nwin = I.t - I.w0 + 1;
+  }
+  I.nsel = max(0, ns);
+  I.ne = (I.nsel + kRows - 1) / kRows;
+  const int tiles = I.ne + (nwin + kRows - 1) / kRows;
+  I.tb = split * tiles / p.nsplit;
+  I.te = (split + 1) * tiles / p.nsplit;
+  return I;
+}
+
+// The tiles of a CTA's items, one after another (empty items skipped).
+struct Stream {
+  Item it;
+  int item, tile;
+  bool live;
+};
+__device__ __forceinline__ void stream_settle(Stream& s, const ChunkTc& p, const int32_t* cu,
+                                              const int32_t* pos0, int lane) {
+  while (s.live && s.tile >= s.it.te) {
+    s.item += gridDim.x;
+    if (s.item >= p.items) { s.live = false; break; }
+    s.it = get_item(p, cu, pos0, s.item, lane);
+    s.live = s.it.live;
+    s.tile = s.it.tb;
+  }
+}
+
+// One lane's row of a tile, resolved in steps so that no step waits for the one before it:
+// the list entry, then the page, then the row's number (-1: no row, zeros).
+struct RowRef {
+  int e, pg;
+  bool window;   // uniform: a window tile (e is already the row's number)
+};
+__device__ __forceinline__ void row_entry(RowRef& r, const Stream& s, const ChunkTc& p, int row) {
+  r.window = false;
+  r.e = -1;
+  r.pg = -1;
+  if (!s.live) return;
+  const Item& I = s.it;
+  if (s.tile < I.ne) {
+    const int pos = s.tile * kRows + row;
+    if (pos < I.nsel) r.e = p.idx ? p.idx[(long long)I.tok * p.k + pos] : pos;
+  } else {
+    r.window = true;
+    const int u = I.w0 + (s.tile - I.ne) * kRows + row;
+    if (u <= I.t) r.e = u >= I.p0 ? kNewTag + I.i0 + (u - I.p0) : I.seq * p.n_w + u % p.n_w;
+  }
+}
+__device__ __forceinline__ void row_page(RowRef& r, int seq, const ChunkTc& p) {
+  if (!r.window && r.e >= 0 && r.e < p.kv.max_pages * kPageEntries)
+    r.pg = p.kv.block_table[(long long)seq * p.kv.max_pages + r.e / kPageEntries];
+}
+__device__ __forceinline__ int row_code(const RowRef& r, const ChunkTc& p) {
+  if (r.window) return r.e;
+  return (unsigned)r.pg < (unsigned)p.kv.num_pages ? r.pg * kPageEntries + r.e % kPageEntries : -1;
+}
+
+// 16 bytes of read-only data that nothing in this CTA reads again.
+__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void sts16(uint8_t* d, uint32_t a, uint32_t b, uint32_t c, uint32_t e) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+               ::"r"(tc::smem_u32(d)), "r"(a), "r"(b), "r"(c), "r"(e) : "memory");
+}
+__device__ __forceinline__ uint8_t* tile_at(uint8_t* sKV, int row, int cb, int cc) {
+  return sKV + cb * kKVBlk + row * 128 + ((cc ^ (row & 7)) << 4);
+}
+
+// bf16 rows.  Warp (quarter qd, half hf) moves rows 32 qd + 16 hf ..+15 of the tile; lane =
+// (row parity, 16-byte chunk of the 128-dim pair).
+__device__ __forceinline__ void load_bf16(uint4 (&st)[24], int slot, int mb, const ChunkTc& p,
+                                          bool window, int code, int hf, int lane) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = __shfl_sync(0xffffffffu, code, 16 * hf + 2 * i + (lane >> 4));
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (c >= 0) {
+      const __nv_bfloat16* base =
+          !window ? static_cast<const __nv_bfloat16*>(p.kv.rows) + (long long)c * kD
+          : c >= kNewTag ? p.new_win + (long long)(c - kNewTag) * kD : p.win + (long long)c * kD;
+      v = ldg_stream(base + 128 * mb + 8 * (lane & 15));
+    }
+    st[8 * slot + i] = v;
+  }
+}
+__device__ __forceinline__ void store_bf16(const uint4 (&st)[24], int slot, int mb, uint8_t* sKV,
+                                           int row0, int lane) {
+  const int c = 16 * mb + (lane & 15);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint4 v = st[8 * slot + i];
+    sts16(tile_at(sKV, row0 + 2 * i + (lane >> 4), c >> 3, c & 7), v.x, v.y, v.z, v.w);
+  }
+}
+
+// FP8 rows: the whole tile in 18 registers of 16 bytes.  Pairs 0-2: lane = (code chunk of 16
+// dims, row), four rows apart in two bits of the lane so that eight lanes store to 128
+// distinct bytes; pair 3: the last 64 codes and the 64 bf16 dims.
+__device__ __forceinline__ void load_fp8(uint4 (&st)[24], uint2& sc, const ChunkTc& p, int code,
+                                         int hf, int lane) {
+  const uint8_t* rows = static_cast<const uint8_t*>(p.kv.rows);
+  const __nv_bfloat16* hi = static_cast<const __nv_bfloat16*>(p.kv.hi);
+  const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+  sc = make_uint2(0u, 0u);
+  if (code >= 0)
+    sc = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.kv.scales) + (long long)code * 8));
+  const int ch = (lane & 3) + ((lane >> 1) & 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = __shfl_sync(0xffffffffu, code, 16 * hf + 4 * i + ((lane >> 2) & 1) + ((lane >> 3) & 2));
+#pragma unroll
+    for (int mb = 0; mb < 3; ++mb)
+      st[4 * mb + i] = c >= 0 ? ldg_stream(rows + (long long)c * kNc + 128 * mb + 16 * ch) : z;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int c = __shfl_sync(0xffffffffu, code, 16 * hf + 8 * i + (lane >> 2));
+    st[12 + i] = c >= 0 ? ldg_stream(rows + (long long)c * kNc + 384 + 16 * (lane & 3)) : z;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = __shfl_sync(0xffffffffu, code, 16 * hf + 4 * i + (lane >> 3));
+    st[14 + i] = c >= 0 ? ldg_stream(hi + (long long)c * kHi + 8 * (lane & 7)) : z;
+  }
+}
+// 16 codes times the scale byte's power of two, as bf16, into chunks cc and cc + 1 of a row.
+__device__ __forceinline__ void store_codes(uint8_t* sKV, int row, int cb, int cc, const uint4& v,
+                                            uint32_t scale_byte) {
+  const float s = scale_value(scale_byte);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float f[4];
+    e4m3x4_scaled(w[i], s, f);
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(f[0], f[1]), hi = __floats2bfloat162_rn(f[2], f[3]);
+    o[2 * i] = *reinterpret_cast<const uint32_t*>(&lo);
+    o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&hi);
+  }
+  sts16(tile_at(sKV, row, cb, cc), o[0], o[1], o[2], o[3]);
+  sts16(tile_at(sKV, row, cb, cc + 1), o[4], o[5], o[6], o[7]);
+}
+__device__ __forceinline__ void store_fp8(const uint4 (&st)[24], const uint2& sc, int mb,
+                                          uint8_t* sKV, int hf, int row0, int lane) {
+  const uint32_t word = mb < 2 ? sc.x : sc.y;   // scales of groups 4 (mb / 2) .. + 3
+  if (mb < 3) {
+    const int ch = (lane & 3) + ((lane >> 1) & 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 4 * i + ((lane >> 2) & 1) + ((lane >> 3) & 2);
+      const uint32_t w = __shfl_sync(0xffffffffu, word, 16 * hf + r);
+      store_codes(sKV, row0 + r, 2 * mb + (ch >> 2), 2 * (ch & 3), st[4 * mb + i],
+                  (w >> (16 * (mb & 1) + 8 * (ch >> 2))) & 0xffu);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 8 * i + (lane >> 2);
+      const uint32_t w = __shfl_sync(0xffffffffu, word, 16 * hf + r);
+      store_codes(sKV, row0 + r, 6, 2 * (lane & 3), st[12 + i], (w >> 16) & 0xffu);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 v = st[14 + i];
+      sts16(tile_at(sKV, row0 + 4 * i + (lane >> 3), 7, lane & 7), v.x, v.y, v.z, v.w);
+    }
+  }
+}
+
+// This thread's part of a pair is in shared memory: publish it to the tensor core and arrive
+// at the pair's barrier (the MMA warp waits there).
+__device__ __forceinline__ void pair_landed(int mb) {
+  tc::fence_proxy_async();
+  tc::tc_fence_before();
+  tc::named_bar_arrive(4 + mb, kThr);
+}
+
+// The query heads of a token into shared memory (cp.async; eight warps, eight heads each).
+__device__ __forceinline__ void load_q(const ChunkTc& p, int tok, uint8_t* sQ, int warp, int lane) {
+  const __nv_bfloat16* qb = p.q + (long long)tok * kH * kD;
+  tc::cp_async_wait_all();   // queries fetched for an item that turned out empty
+  for (int h = warp; h < kH; h += kSW) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int c = lane + 32 * x;
+      tc::cp_async16(sQ + (c >> 3) * kQBlk + h * 128 + (((c & 7) ^ (h & 7)) << 4), qb + (long long)h * kD + 8 * c, 16);
+    }
+  }
+}
+
+__device__ __forceinline__ float nan_f() { return __int_as_float(0x7fc00000); }
+
+// Weight of rows with reference maximum M (log2 units) and of the sink in a denominator
+// taken relative to top = max(M, sink2); neither is NaN when one or both are -inf.
+__device__ __forceinline__ float rel_weight(float x, float top) {
+  return x == -INFINITY ? 0.f : x == top ? 1.f : exp2f(x - top);
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(kLaunch, 1) chunk_tc_kernel(ChunkTc p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* sKV = base;                            // 8 x 16 KB
+  uint8_t* sQ = sKV + 8 * kKVBlk;                 // 8 x 8 KB
+  uint8_t* sP = sQ + 8 * kQBlk;                   // 16 KB
+  float* s_red = reinterpret_cast<float*>(sP + kRows * 128);   // [4][64]
+  float* s_M = s_red + 4 * kH;                    // running reference maximum, log2 units
+  float* s_Mu = s_M + kH;                         // the same, 0 where it is -inf
+  float* s_alpha = s_Mu + kH;
+  float* s_sink2 = s_alpha + kH;
+  int* s_flag = reinterpret_cast<int*>(s_sink2 + kH);
+  uint64_t* bar_s = reinterpret_cast<uint64_t*>(s_flag + 4);
+  uint64_t* bar_pv = bar_s + 1;                   // [4]
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bar_pv + 4);
+  int32_t* s_cu = reinterpret_cast<int32_t*>(tmem_holder + 2);   // [kSeqCache + 1]
+  int32_t* s_pos0 = s_cu + kSeqCache + 1;         // [kSeqCache]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_launch_dependents();
+  const bool cached = p.b <= kSeqCache;
+  if (cached) {
+    for (int i = tid; i <= p.b; i += kLaunch) s_cu[i] = p.cu_q[i];
+    for (int i = tid; i < p.b; i += kLaunch) s_pos0[i] = p.pos0[i];
+  }
+  const int32_t* cu = cached ? s_cu : p.cu_q;
+  const int32_t* pos0 = cached ? s_pos0 : p.pos0;
+  if (tid < kH) s_sink2[tid] = p.sink[tid] * kLog2e;
+  if (tid == 0) {
+    tc::mbar_init(bar_s, 1);
+    for (int i = 0; i < 4; ++i) tc::mbar_init(bar_pv + i, 1);
+    tc::fence_barrier_init();
+  }
+  if (warp == 0) tc::tmem_alloc(tmem_holder, 512);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const uint32_t tS = tmem, tO = tmem + 64;       // columns [0, 64) S^T; [64, 320) O^T
+
+  if (warp >= kSW) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
+    // ------------------------------------------------------------------ MMA issuer
+    if (warp == kSW) {
+    constexpr uint32_t idS = tc::instr_desc(128, kH, 1, 1, 0, 0);   // K-major x K-major
+    constexpr uint32_t idO = tc::instr_desc(128, kH, 1, 1, 1, 1);   // MN-major x MN-major
+    const uint64_t dS_a = tc::smem_desc_sw128(tc::smem_u32(sKV), 16, 1024);
+    const uint64_t dS_b = tc::smem_desc_sw128(tc::smem_u32(sQ), 16, 1024);
+    const uint64_t dO_a = tc::smem_desc_sw128(tc::smem_u32(sKV), kKVBlk, 1024);
+    const uint64_t dO_b = tc::smem_desc_sw128(tc::smem_u32(sP), 8192, 1024);
+    for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
+      const Item I = get_item(p, cu, pos0, item, lane);
+      if (!I.live) break;
+      for (int j = I.tb; j < I.te; ++j) {
+        for (int mb = 0; mb < 4; ++mb) {
+          tc::named_bar(4 + mb, kThr);             // the pair (and, with the first, q) is in place
+          if (lane == 0) {
+            tc::tc_fence_after();
+#pragma unroll
+            for (int kb = 2 * mb; kb < 2 * mb + 2; ++kb) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                tc::mma_f16(tS, tc::desc_advance(dS_a, kb * kKVBlk + kk * 32),
+                            tc::desc_advance(dS_b, kb * kQBlk + kk * 32), idS, (kb | kk) != 0);
+            }
+            if (mb == 3) tc::mma_commit(bar_s);
+          }
+          __syncwarp();
+        }
+        tc::named_bar(2, kThr);                    // P^T in place, O^T rescaled
+        if (lane == 0) {
+          tc::tc_fence_after();
+#pragma unroll
+          for (int mb = 0; mb < 4; ++mb) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              tc::mma_f16(tO + mb * kH, tc::desc_advance(dO_a, 2 * mb * kKVBlk + kk * 2048),
+                          tc::desc_advance(dO_b, kk * 2048), idO, (j > I.tb) || (kk > 0));
+            tc::mma_commit(bar_pv + mb);           // column blocks 2 mb, 2 mb + 1 are free
+          }
+        }
+        __syncwarp();
+      }
+    }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    // ------------------------------------------------------------------ gather and softmax
+    const int qd = warp & 3, hf = warp >> 2;
+    const int row = qd * 32 + lane;                // TMEM lane = tile row of this thread
+    const int row0 = qd * 32 + 16 * hf;            // first of the 16 rows this warp moves
+    const uint32_t lane_addr = (uint32_t)(qd * 32) << 16;
+    uint32_t ns = 0, npv = 0;                      // phases of bar_s and bar_pv waited for
+    bool ok = true, pv_pending = false;
+    int q_item = -1;                               // item whose queries are in sQ or on their way
+
+    uint4 st[24];
+    uint2 sc = make_uint2(0u, 0u);
+    Stream S;
+    S.item = blockIdx.x;
+    S.live = S.item < p.items;
+    S.it.te = 0; S.tile = 0;
+    if (S.live) {
+      S.it = get_item(p, cu, pos0, S.item, lane);
+      S.live = S.it.live;
+      S.tile = S.it.tb;
+      if (S.live && S.it.te > S.it.tb) {
+        load_q(p, S.it.tok, sQ, warp, lane);
+        q_item = S.item;
+      }
+      stream_settle(S, p, cu, pos0, lane);
+    }
+    // the first tile's rows and loads, then the second tile's list entries and pages
+    RowRef nx;
+    row_entry(nx, S, p, row);
+    row_page(nx, S.it.seq, p);
+    int code = row_code(nx, p);
+    bool window = nx.window;
+    auto issue = [&]() {
+      if (FP8 && !window) {
+        load_fp8(st, sc, p, code, hf, lane);
+      } else {
+#pragma unroll
+        for (int mb = 0; mb < 3; ++mb) load_bf16(st, mb, mb, p, window, code, hf, lane);
+      }
+    };
+    if (S.live) {
+      issue();
+      ++S.tile;
+      stream_settle(S, p, cu, pos0, lane);
+      row_entry(nx, S, p, row);
+      row_page(nx, S.it.seq, p);
+    }
+
+    for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
+      const Item I = get_item(p, cu, pos0, item, lane);
+      if (!I.live) break;
+      float lsum[32];
+#pragma unroll
+      for (int h = 0; h < 32; ++h) lsum[h] = 0.f;
+      if (I.te > I.tb && q_item != item) {
+        load_q(p, I.tok, sQ, warp, lane);
+        q_item = item;
+      }
+      for (int j = I.tb; j < I.te; ++j) {
+        // the staged tile into shared memory, pair by pair as the previous PV frees the pairs
+#pragma unroll
+        for (int mb = 0; mb < 4; ++mb) {
+          if (pv_pending) {
+            ok = ok && tc::mbar_wait_hint(bar_pv + mb, npv & 1, p.err, kHintNs);
+            tc::tc_fence_after();
+          }
+          if (FP8 && !window) store_fp8(st, sc, mb, sKV, hf, row0, lane);
+          else store_bf16(st, mb == 3 ? 0 : mb, mb, sKV, row0, lane);
+          if (mb == 0) {
+            if (!(FP8 && !window)) load_bf16(st, 0, 3, p, window, code, hf, lane);
+            if (j == I.tb) tc::cp_async_wait_all();   // the queries
+          }
+          pair_landed(mb);
+        }
+        if (pv_pending) ++npv;
+        const bool valid = code >= 0;
+        const bool last = j == I.te - 1;
+        // the next tile's loads, and the list entries of the one after it
+        const bool more = S.live;
+        if (more) {
+          code = row_code(nx, p);
+          window = nx.window;
+          issue();
+          ++S.tile;
+          stream_settle(S, p, cu, pos0, lane);
+          row_entry(nx, S, p, row);
+        }
+
+        ok = ok && tc::mbar_wait_hint(bar_s, ns & 1, p.err, kHintNs);
+        ++ns;
+        tc::tc_fence_after();
+        if (last && item + (int)gridDim.x < p.items) {
+          // S^T was the last reader of these queries: fetch the next item's
+          const int tok = (item + (int)gridDim.x) / p.nsplit;
+          if (tok < cu[p.b]) {
+            load_q(p, tok, sQ, warp, lane);
+            q_item = item + (int)gridDim.x;
+          }
+        }
+        uint32_t lg[32];                           // logits (float bits), log2 units
+        auto logits = [&]() {
+          tc::tmem_ld32(tS + lane_addr + 32 * hf, lg);
+          tc::tmem_ld_wait(lg);
+#pragma unroll
+          for (int h = 0; h < 32; ++h)
+            lg[h] = __float_as_uint(valid ? __uint_as_float(lg[h]) * p.scale_log2 : -INFINITY);
+        };
+        logits();
+        bool exact = j == I.tb;
+        if (!exact) {
+          bool big = false;
+#pragma unroll
+          for (int h = 0; h < 32; h += 4) {
+            const float4 M4 = *reinterpret_cast<const float4*>(s_M + 32 * hf + h);
+            big |= __uint_as_float(lg[h]) > M4.x + kRescale;
+            big |= __uint_as_float(lg[h + 1]) > M4.y + kRescale;
+            big |= __uint_as_float(lg[h + 2]) > M4.z + kRescale;
+            big |= __uint_as_float(lg[h + 3]) > M4.w + kRescale;
+          }
+          exact = tc::bar_red_or(3, kST, big);
+        }
+        if (exact) {
+          // the reduction consumes the logits, which are read from TMEM again below (keeping
+          // them beside it would not fit the registers)
+          {
+            float v[32];
+#pragma unroll
+            for (int h = 0; h < 32; ++h) v[h] = __uint_as_float(lg[h]);
+            xpose_reduce32<true>(v, lane);
+            if (tid == 0) s_flag[0] = 0;           // its last reads are behind two barriers
+            s_red[qd * kH + 32 * hf + lane] = v[0];
+          }
+          tc::named_bar(3, kST);
+          if (tid < kH) {
+            const float tm = fmaxf(fmaxf(s_red[tid], s_red[kH + tid]), fmaxf(s_red[2 * kH + tid], s_red[3 * kH + tid]));
+            const float Mr = s_M[tid];
+            float Mn = Mr, al = 1.f;
+            if (j == I.tb) {
+              Mn = tm;
+            } else if (tm > Mr + kRescale) {
+              Mn = tm;
+              al = exp2f(Mr - tm);
+              s_flag[0] = 1;
+            }
+            s_M[tid] = Mn;
+            s_Mu[tid] = Mn == -INFINITY ? 0.f : Mn;   // a tile without rows gives p = 0, not NaN
+            s_alpha[tid] = al;
+          }
+          tc::named_bar(3, kST);
+          if (j > I.tb && s_flag[0]) {
+            for (int mb = 2 * hf; mb < 2 * hf + 2; ++mb) {
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                uint32_t o[32];
+                const uint32_t ta = tO + mb * kH + half * 32 + lane_addr;
+                tc::tmem_ld32(ta, o);
+                tc::tmem_ld_wait(o);
+#pragma unroll
+                for (int h = 0; h < 32; ++h)
+                  o[h] = __float_as_uint(__uint_as_float(o[h]) * s_alpha[half * 32 + h]);
+                tc::tmem_st32(ta, o);
+              }
+            }
+            tc::tmem_st_wait();
+#pragma unroll
+            for (int h = 0; h < 32; ++h) lsum[h] *= s_alpha[32 * hf + h];
+          }
+          logits();
+        }
+        // probabilities: bf16 into P^T (this row's 128-byte line, four 16-byte chunks of it);
+        // the sums take them before that rounding
+#pragma unroll
+        for (int cb = 0; cb < 4; ++cb) {
+          uint32_t w4[4];
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const int h = cb * 8 + 2 * e;
+            const float4 M4 = *reinterpret_cast<const float4*>(s_Mu + 32 * hf + h);
+            const float p0 = exp2f(__uint_as_float(lg[h]) - M4.x), p1 = exp2f(__uint_as_float(lg[h + 1]) - M4.y);
+            const float p2 = exp2f(__uint_as_float(lg[h + 2]) - M4.z), p3 = exp2f(__uint_as_float(lg[h + 3]) - M4.w);
+            lsum[h] += p0; lsum[h + 1] += p1; lsum[h + 2] += p2; lsum[h + 3] += p3;
+            const __nv_bfloat162 a = __floats2bfloat162_rn(p0, p1), b2 = __floats2bfloat162_rn(p2, p3);
+            w4[e] = *reinterpret_cast<const uint32_t*>(&a);
+            w4[e + 1] = *reinterpret_cast<const uint32_t*>(&b2);
+          }
+          sts16(sP + row * 128 + (((4 * hf + cb) ^ (row & 7)) << 4), w4[0], w4[1], w4[2], w4[3]);
+        }
+        tc::fence_proxy_async();
+        tc::tc_fence_before();
+        tc::named_bar_arrive(2, kThr);
+        pv_pending = true;
+        if (more) row_page(nx, S.it.seq, p);
+      }
+
+      // ---------------------------------------------------------------- the item's output
+      if (I.te <= I.tb) {
+        if (p.nsplit > 1) {                        // nothing to add: weight 0, O not written
+          if (tid < kH) {
+            p.part_m[(long long)item * kH + tid] = -INFINITY;
+            p.part_l[(long long)item * kH + tid] = 0.f;
+          }
+        } else {
+          uint4* o = reinterpret_cast<uint4*>(p.out + (long long)I.tok * kH * kD);
+          for (int x = tid; x < kH * kD / 8; x += kST) o[x] = make_uint4(0u, 0u, 0u, 0u);
+          if (p.lse && tid < kH) p.lse[(long long)I.tok * kH + tid] = s_sink2[tid] * kLn2;
+        }
+        continue;
+      }
+      xpose_reduce32<false>(lsum, lane);
+      tc::named_bar(3, kST);                       // s_red's readers of the last maximum are done
+      s_red[qd * kH + 32 * hf + lane] = lsum[0];
+      tc::named_bar(3, kST);
+      if (tid < kH) {
+        const float l = s_red[tid] + s_red[kH + tid] + s_red[2 * kH + tid] + s_red[3 * kH + tid];
+        const float M = s_M[tid];
+        if (p.nsplit > 1) {
+          p.part_m[(long long)item * kH + tid] = M;
+          p.part_l[(long long)item * kH + tid] = l;
+        } else {
+          const float sink2 = s_sink2[tid], top = fmaxf(M, sink2);
+          const float wr = rel_weight(M, top);
+          const float den = l * wr + rel_weight(sink2, top);
+          s_alpha[tid] = den == 0.f ? 0.f : wr / den;
+          if (p.lse) p.lse[(long long)I.tok * kH + tid] = den == 0.f ? -INFINITY : (top + log2f(den)) * kLn2;
+        }
+      }
+      tc::named_bar(3, kST);
+      if (p.nsplit > 1) {
+        for (int mb = 2 * hf; mb < 2 * hf + 2; ++mb) {
+          ok = ok && tc::mbar_wait_hint(bar_pv + mb, npv & 1, p.err, kHintNs);
+          tc::tc_fence_after();
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t o[32];
+            tc::tmem_ld32(tO + mb * kH + half * 32 + lane_addr, o);
+            tc::tmem_ld_wait(o);
+            float4* dst = reinterpret_cast<float4*>(p.part_o + ((long long)item * kD + mb * 128 + row) * kH + half * 32);
+#pragma unroll
+            for (int h4 = 0; h4 < 8; ++h4)
+              dst[h4] = ok ? make_float4(__uint_as_float(o[4 * h4]), __uint_as_float(o[4 * h4 + 1]),
+                                         __uint_as_float(o[4 * h4 + 2]), __uint_as_float(o[4 * h4 + 3]))
+                           : make_float4(nan_f(), nan_f(), nan_f(), nan_f());
+          }
+        }
+        // the pairs this half did not wait for: the next tile may overwrite all four
+        for (int mb = 2 - 2 * hf; mb < 4 - 2 * hf; ++mb)
+          ok = ok && tc::mbar_wait_hint(bar_pv + mb, npv & 1, p.err, kHintNs);
+      } else {
+        for (int mb = 0; mb < 4; ++mb) {
+          ok = ok && tc::mbar_wait_hint(bar_pv + mb, npv & 1, p.err, kHintNs);
+          tc::tc_fence_after();
+          uint32_t o[32];
+          tc::tmem_ld32(tO + mb * kH + 32 * hf + lane_addr, o);
+          tc::tmem_ld_wait(o);
+          // lanes 2i and 2i + 1 hold dims 2i and 2i + 1 of every head: the even lane takes both
+          // of head h, the odd one both of head h + 1, for 4-byte stores and the rotary pair
+          const int d = mb * 128 + (row & ~1);
+          const bool rot = d >= kD - p.d_rope_out;
+          float sn = 0.f, cs = 1.f;
+          if (rot) rope_angle((double)I.t * p.inv_freq[(d - (kD - p.d_rope_out)) >> 1], &sn, &cs);
+#pragma unroll
+          for (int h = 0; h < 32; h += 2) {
+            const float2 w = *reinterpret_cast<const float2*>(s_alpha + 32 * hf + h);
+            const float a = w.x == 0.f ? 0.f : __uint_as_float(o[h]) * w.x;
+            const float c = w.y == 0.f ? 0.f : __uint_as_float(o[h + 1]) * w.y;
+            const bool odd = lane & 1;
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? a : c, 1);
+            float x0 = odd ? got : a, x1 = odd ? c : got;
+            if (rot) {
+              const float y0 = fmaf(x0, cs, x1 * sn), y1 = fmaf(x1, cs, -x0 * sn);
+              x0 = y0; x1 = y1;
+            }
+            if (!ok) x0 = x1 = nan_f();
+            *reinterpret_cast<__nv_bfloat162*>(
+                p.out + ((long long)I.tok * kH + 32 * hf + h + (odd ? 1 : 0)) * kD + d) =
+                __floats2bfloat162_rn(x0, x1);
+          }
+        }
+      }
+      ++npv;
+      pv_pending = false;
+      tc::tc_fence_before();
+      tc::named_bar(3, kST);                       // s_red, s_alpha and s_M are free again
+    }
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// Combines the splits of a token: CTA per (token, 16 dims), thread per (head, 4 dims).  The
+// weights e^(m_s - top) / den of every split come first, then each thread adds its four dims
+// over the splits (coalesced over the heads).
+constexpr int kMergeDims = 16;
+__global__ void __launch_bounds__(256) chunk_merge_kernel(ChunkTc p) {
+  __shared__ float s_w[kMaxSplit][kH];
+  const int tok = blockIdx.x, tid = threadIdx.x;
+  const int h = tid & (kH - 1), d = blockIdx.y * kMergeDims + 4 * (tid >> 6);
+  const int seq = find_seq(p.cu_q, p.b, tok, tid & 31);
+  if (seq >= p.b || tok < p.cu_q[0]) return;
+  const int t = p.pos0[seq] + (tok - p.cu_q[seq]);
+  const float sink2 = p.sink[h] * kLog2e;
+  pdl_wait();
+  const long long it0 = (long long)tok * p.nsplit;
+  if (tid < kH) {
+    float top = sink2;
+    for (int s = 0; s < p.nsplit; ++s) top = fmaxf(top, p.part_m[(it0 + s) * kH + h]);
+    float den = rel_weight(sink2, top);
+    for (int s = 0; s < p.nsplit; ++s) {
+      const float w = rel_weight(p.part_m[(it0 + s) * kH + h], top);
+      s_w[s][h] = w;
+      den = fmaf(p.part_l[(it0 + s) * kH + h], w, den);
+    }
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    for (int s = 0; s < p.nsplit; ++s) s_w[s][h] *= inv;
+    if (p.lse && blockIdx.y == 0)
+      p.lse[(long long)tok * kH + h] = den == 0.f ? -INFINITY : (top + log2f(den)) * kLn2;
+  }
+  __syncthreads();
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < p.nsplit; ++s) {
+    const float w = s_w[s][h];
+    if (w == 0.f) continue;                        // an empty split's O is not written
+    const float* src = p.part_o + ((it0 + s) * kD + d) * kH + h;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) acc[u] = fmaf(src[u * kH], w, acc[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < 4; u += 2) {
+    const int x = d + u - (kD - p.d_rope_out);
+    if (x >= 0 && p.d_rope_out > 0) {
+      float sn, cs;
+      rope_angle((double)t * p.inv_freq[x >> 1], &sn, &cs);
+      const float y0 = fmaf(acc[u], cs, acc[u + 1] * sn), y1 = fmaf(acc[u + 1], cs, -acc[u] * sn);
+      acc[u] = y0; acc[u + 1] = y1;
+    }
+  }
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[0], acc[1]), hi = __floats2bfloat162_rn(acc[2], acc[3]);
+  uint2 v;
+  v.x = *reinterpret_cast<const uint32_t*>(&lo);
+  v.y = *reinterpret_cast<const uint32_t*>(&hi);
+  *reinterpret_cast<uint2*>(p.out + ((long long)tok * kH + h) * kD + d) = v;
+}
+
+constexpr size_t kSmem = 1024 + 8 * kKVBlk + 8 * kQBlk + kRows * 128 + (4 * kH + 4 * kH) * 4 + 16 + 5 * 8 + 8 +
+                         (2 * kSeqCache + 1) * 4;
+static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+
+int sm_count() {
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+// Splits per token.  A CTA's time for an item of n tiles is about n + 1.5 tiles (queries,
+// the first tile's latency, the output); the CTAs work through ceil(N splits / SMs) items
+// each; a merge costs about three tiles.
+int plan_splits(int n_w, int m, int k, int N, int L_max) {
+  const int E = k > 0 ? k : L_max / m;
+  const int tiles = (E + kRows - 1) / kRows + (n_w + kRows - 1) / kRows;
+  const int sms = sm_count();
+  int best = 1;
+  double least = 0;
+  for (int ns = 1; ns <= std::min(kMaxSplit, std::max(tiles, 1)); ++ns) {
+    const double rounds = (double)(((long long)N * ns + sms - 1) / sms);
+    const double cost = rounds * ((tiles + ns - 1) / ns + 1.5) + (ns > 1 ? 3.0 : 0.0);
+    if (ns == 1 || cost < least) { best = ns; least = cost; }
+  }
+  return best;
+}
+
+}  // namespace
+
+bool chunk_tc_supported(int H, int d, int dtype, int d_rope_out, const csa_kv_cache& kv) {
+  if (H != kH || d != kD || dtype != CSA_BF16 || d_rope_out > 2 * kMaxOutRopePairs) return false;
+  if ((long long)kv.num_pages * kPageEntries > INT_MAX) return false;
+  return kv.dtype == CSA_BF16 || (kv.dtype == CSA_FP8_E4M3 && kv.d_hi == kHi);
+}
+
+int chunk_tc_launch_count(int n_w, int m, int k, int N, int L_max) {
+  return plan_splits(n_w, m, k, N, L_max) > 1 ? 2 : 1;
+}
+
+size_t chunk_tc_workspace_bytes(int n_w, int m, int k, int N, int L_max) {
+  const int ns = plan_splits(n_w, m, k, N, L_max);
+  return ns > 1 ? (size_t)N * ns * kH * (kD + 2) * 4 : 0;
+}
+
+csa_status launch_chunk_attn_tc(const ChunkArgs& a, const csa_kv_cache& kv, void* ws,
+                                size_t ws_bytes, cudaStream_t st) {
+  // row numbers of the window and of q carry a tag in bit 30
+  if ((long long)a.b * a.n_w >= kNewTag || a.N >= kNewTag) return CSA_ERR_UNSUPPORTED;
+  ChunkTc p{};
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.win = static_cast<const __nv_bfloat16*>(a.win);
+  p.new_win = static_cast<const __nv_bfloat16*>(a.new_win);
+  p.cu_q = a.cu_q; p.pos0 = a.pos0; p.idx = a.idx; p.count = a.count; p.sink = a.sink;
+  p.out = static_cast<__nv_bfloat16*>(a.out); p.lse = a.lse; p.kv = kv;
+  p.b = a.b; p.N = a.N; p.n_w = a.n_w; p.m = a.m; p.k = a.k; p.d_rope_out = a.d_rope_out;
+  p.scale_log2 = a.scale * kLog2e;
+  p.err = device_error_word();
+  if (!p.err) return CSA_ERR_CUDA;
+  for (int j = 0; j < kMaxOutRopePairs; ++j)
+    p.inv_freq[j] = 2 * j < a.d_rope_out ? std::pow(a.theta, -2.0 * j / (double)a.d_rope_out) : 0.0;
+  p.nsplit = plan_splits(a.n_w, a.m, a.k, a.N, a.L_max);
+  const long long items = (long long)a.N * p.nsplit;
+  if (items > INT_MAX) return CSA_ERR_UNSUPPORTED;
+  p.items = (int)items;
+  if (p.nsplit > 1) {
+    if (!ws || ws_bytes < (size_t)items * kH * (kD + 2) * 4 || (reinterpret_cast<uintptr_t>(ws) & 15))
+      return CSA_ERR_INVALID_ARG;
+    p.part_o = static_cast<float*>(ws);
+    p.part_m = p.part_o + items * kH * kD;
+    p.part_l = p.part_m + items * kH;
+  }
+  auto kern = kv.dtype == CSA_FP8_E4M3 ? chunk_tc_kernel<true> : chunk_tc_kernel<false>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
+    return CSA_ERR_CUDA;
+  const int grid = (int)std::min<long long>(items, sm_count());
+  if (csa_launch(kern, dim3(grid), dim3(kLaunch), kSmem, st, false, p) != cudaSuccess) return CSA_ERR_CUDA;
+  if (p.nsplit > 1 &&
+      csa_launch(chunk_merge_kernel, dim3(a.N, kD / kMergeDims), dim3(256), 0, st, true, p) != cudaSuccess)
+    return CSA_ERR_CUDA;
+  return CSA_OK;
+}
+
 }  // namespace csa
