@@ -15,16 +15,21 @@
 // What bounds it: the two products of a tile take ~3,200 cycles (at N = 64 an MMA reads 6 KB
 // of operands, 48 cycles at 128 bytes a cycle, for 32 cycles of math), and one tile of
 // shared memory (128 KB, beside 64 KB of queries) leaves no room for a second.  So the next
-// tile waits in registers: as soon as a tile has been stored, every softmax thread issues the
-// loads of its share of the next one (three of the four 128-dim pairs in bf16, all of it in
-// FP8), which travel under this tile's softmax and PV; each pair is stored the moment the PV
-// has read its predecessor, and its S^T MMAs start on it.  FP8 rows become bf16 on the way
-// to shared memory (code times a power of two: exact).
+// tile waits in registers: producer warps issue its loads as soon as the current tile is
+// stored (two of its four 128-dim pairs in bf16, three in FP8), they travel under this
+// tile's softmax and PV, and each pair is stored the moment the PV has read its predecessor;
+// its S^T MMAs start on it.  FP8 rows become bf16 on the way to shared memory (code times a
+// power of two: exact).  Loads and softmax in the same warps made a tile 10,400 cycles, since
+// the softmax's shuffles and shared-memory accesses queued behind the loads.
 //
 // The softmax keeps the maximum lazily (raised only when a tile exceeds it by 2^8, which
 // rescales O^T in TMEM) and each thread's sums of its 32 heads in registers over the tiles of
 // an item: the reduction over the rows runs once per item, so an ordinary tile needs one
 // barrier (the OR of "some logit exceeds the maximum") before its probabilities.
+//
+// CTA: warps 0-7 softmax and output (two per TMEM lane quarter, 32 heads each), warps 8-11
+// producers, warp 12 issues every MMA (13-15 idle: register shares go by warpgroup).
+// Producers walk the CTA's tiles as one stream across its items.
 //
 // Work item = (token, split of its tiles); CTAs walk the items with stride gridDim.x.  Few
 // tokens are split over several CTAs (fp32 partials, combined by chunk_merge_kernel), many
@@ -52,15 +57,19 @@ constexpr int kQBlk = kH * 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;      // log2 units
-constexpr int kSW = 8;                // softmax / gather warps: two per TMEM lane quarter
+constexpr int kSW = 8;                // softmax warps
+constexpr int kPW = 4;                // producer warps, one per quarter of a tile's rows
 constexpr int kST = 32 * kSW;
-constexpr int kThr = kST + 32;        // plus the MMA warp: the threads of the tile barriers
-// The CTA is launched with three whole warpgroups (the MMA warp and three that idle make the
-// third) of 168 registers a thread, the most that fits; the third hands most of its share to
-// the other two, which hold a tile in registers: 2 x 216 + 72 = 3 x 168.
-constexpr int kLaunch = 384;
-constexpr int kRegsSoftmax = 216, kRegsMma = 72;
-static_assert(2 * kRegsSoftmax + kRegsMma <= 3 * 168, "setmaxnreg shares");
+constexpr int kBarS = kST + 32;       // threads of a barrier of the softmax and the MMA warp
+constexpr int kBarP = 32 * kPW + 32;  // ... of the producers and the MMA warp
+constexpr int kLaunch = 512;
+// Registers a thread by warpgroup (2 x softmax, producers, MMA), out of 4 x 128 at launch.
+constexpr int kRegsSoftmax = 112, kRegsProd = 208, kRegsMma = 80;
+constexpr int kRegsLaunch = 128;      // 65,536 / 512
+// .dec must not raise a warpgroup's count and .inc must not lower it (either faults), and the
+// shares must fit what the block was launched with (or .inc waits for good).
+static_assert(kRegsSoftmax <= kRegsLaunch && kRegsMma <= kRegsLaunch && kRegsProd >= kRegsLaunch &&
+                  2 * kRegsSoftmax + kRegsProd + kRegsMma <= 4 * kRegsLaunch, "setmaxnreg shares");
 constexpr uint32_t kHintNs = 64;
 constexpr int kSeqCache = 1024;       // sequences whose boundaries are kept in shared memory
 constexpr int kMaxSplit = 32;
@@ -162,12 +171,20 @@ __device__ __forceinline__ int row_code(const RowRef& r, const ChunkTc& p) {
   return (unsigned)r.pg < (unsigned)p.kv.num_pages ? r.pg * kPageEntries + r.e % kPageEntries : -1;
 }
 
-// 16 bytes of read-only data that nothing in this CTA reads again.
-__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+// 16 bytes of read-only data that nothing in this CTA reads again; zeros where !have.
+__device__ __forceinline__ uint4 ldg_stream(const void* p, bool have) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"((uint32_t)have));
   return v;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 __device__ __forceinline__ void sts16(uint8_t* d, uint32_t a, uint32_t b, uint32_t c, uint32_t e) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
@@ -177,66 +194,76 @@ __device__ __forceinline__ uint8_t* tile_at(uint8_t* sKV, int row, int cb, int c
   return sKV + cb * kKVBlk + row * 128 + ((cc ^ (row & 7)) << 4);
 }
 
-// bf16 rows.  Warp (quarter qd, half hf) moves rows 32 qd + 16 hf ..+15 of the tile; lane =
-// (row parity, 16-byte chunk of the 128-dim pair).
-__device__ __forceinline__ void load_bf16(uint4 (&st)[24], int slot, int mb, const ChunkTc& p,
-                                          bool window, int code, int hf, int lane) {
+constexpr int kStage = 32;   // 16-byte registers a producer thread stages of the next tile
+
+// bf16 rows: producer warp qd moves rows 32 qd ..+31 of the tile; lane = (row parity, 16-byte
+// chunk of a 128-dim pair).  `src` is the address of this lane's row of the quarter (0: none).
+// Two of the four pairs are staged; the other two are loaded into their registers as those
+// are stored.
+__device__ __forceinline__ void load_bf16(uint4 (&st)[kStage], int mb0, int nmb, uint64_t src, int lane) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int c = __shfl_sync(0xffffffffu, code, 16 * hf + 2 * i + (lane >> 4));
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (c >= 0) {
-      const __nv_bfloat16* base =
-          !window ? static_cast<const __nv_bfloat16*>(p.kv.rows) + (long long)c * kD
-          : c >= kNewTag ? p.new_win + (long long)(c - kNewTag) * kD : p.win + (long long)c * kD;
-      v = ldg_stream(base + 128 * mb + 8 * (lane & 15));
-    }
-    st[8 * slot + i] = v;
+  for (int i = 0; i < 16; ++i) {
+    const uint64_t row = __shfl_sync(0xffffffffu, src, 2 * i + (lane >> 4));
+    const char* a = reinterpret_cast<const char*>(row) + 16 * (lane & 15);
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      if (x < nmb) st[16 * ((mb0 + x) & 1) + i] = ldg_stream(a + 256 * (mb0 + x), row != 0);
   }
 }
-__device__ __forceinline__ void store_bf16(const uint4 (&st)[24], int slot, int mb, uint8_t* sKV,
-                                           int row0, int lane) {
+__device__ __forceinline__ void store_bf16(const uint4 (&st)[kStage], int mb, uint8_t* sKV, int row0,
+                                           int lane) {
   const int c = 16 * mb + (lane & 15);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint4 v = st[8 * slot + i];
+  for (int i = 0; i < 16; ++i) {
+    const uint4 v = st[16 * (mb & 1) + i];
     sts16(tile_at(sKV, row0 + 2 * i + (lane >> 4), c >> 3, c & 7), v.x, v.y, v.z, v.w);
   }
 }
+// Address of a plain row: in the pool, in new_win or in the rings.
+__device__ __forceinline__ uint64_t row_addr(const ChunkTc& p, bool window, int code) {
+  if (code < 0) return 0;
+  const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(p.kv.rows);
+  if (window) {
+    base = code >= kNewTag ? p.new_win : p.win;
+    code &= kNewTag - 1;
+  }
+  return reinterpret_cast<uint64_t>(base + (long long)code * kD);
+}
 
-// FP8 rows: the whole tile in 18 registers of 16 bytes.  Pairs 0-2: lane = (code chunk of 16
-// dims, row), four rows apart in two bits of the lane so that eight lanes store to 128
-// distinct bytes; pair 3: the last 64 codes and the 64 bf16 dims.
-__device__ __forceinline__ void load_fp8(uint4 (&st)[24], uint2& sc, const ChunkTc& p, int code,
-                                         int hf, int lane) {
+// FP8 rows: pairs 0-2 are staged, lane = (code chunk of 16 dims, row), the row in three bits
+// of the lane so that eight lanes store to 128 distinct bytes; pair 3 (the last 64 codes and
+// the 64 bf16 dims) is loaded into the registers of pairs 0 and 1 as those are stored.
+__device__ __forceinline__ int fp8_row(int i, int lane) { return 4 * i + ((lane >> 2) & 1) + ((lane >> 3) & 2); }
+__device__ __forceinline__ int fp8_chunk(int lane) { return (lane & 3) + ((lane >> 1) & 4); }
+__device__ __forceinline__ void load_fp8(uint4 (&st)[kStage], uint2& sc, const ChunkTc& p, int code, int lane) {
   const uint8_t* rows = static_cast<const uint8_t*>(p.kv.rows);
-  const __nv_bfloat16* hi = static_cast<const __nv_bfloat16*>(p.kv.hi);
-  const uint4 z = make_uint4(0u, 0u, 0u, 0u);
   sc = make_uint2(0u, 0u);
   if (code >= 0)
     sc = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.kv.scales) + (long long)code * 8));
-  const int ch = (lane & 3) + ((lane >> 1) & 4);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = __shfl_sync(0xffffffffu, code, 16 * hf + 4 * i + ((lane >> 2) & 1) + ((lane >> 3) & 2));
+  for (int i = 0; i < 8; ++i) {
+    const int c = __shfl_sync(0xffffffffu, code, fp8_row(i, lane));
+    const uint8_t* a = rows + (long long)c * kNc + 16 * fp8_chunk(lane);
 #pragma unroll
-    for (int mb = 0; mb < 3; ++mb)
-      st[4 * mb + i] = c >= 0 ? ldg_stream(rows + (long long)c * kNc + 128 * mb + 16 * ch) : z;
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int c = __shfl_sync(0xffffffffu, code, 16 * hf + 8 * i + (lane >> 2));
-    st[12 + i] = c >= 0 ? ldg_stream(rows + (long long)c * kNc + 384 + 16 * (lane & 3)) : z;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = __shfl_sync(0xffffffffu, code, 16 * hf + 4 * i + (lane >> 3));
-    st[14 + i] = c >= 0 ? ldg_stream(hi + (long long)c * kHi + 8 * (lane & 7)) : z;
+    for (int mb = 0; mb < 3; ++mb) st[8 * mb + i] = ldg_stream(a + 128 * mb, c >= 0);
   }
 }
-// 16 codes times the scale byte's power of two, as bf16, into chunks cc and cc + 1 of a row.
-__device__ __forceinline__ void store_codes(uint8_t* sKV, int row, int cb, int cc, const uint4& v,
-                                            uint32_t scale_byte) {
+__device__ __forceinline__ void load_fp8_last(uint4 (&st)[kStage], const ChunkTc& p, int code, int lane) {
+  const uint8_t* rows = static_cast<const uint8_t*>(p.kv.rows);
+  const __nv_bfloat16* hi = static_cast<const __nv_bfloat16*>(p.kv.hi);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = __shfl_sync(0xffffffffu, code, 8 * i + (lane >> 2));
+    st[i] = ldg_stream(rows + (long long)c * kNc + 384 + 16 * (lane & 3), c >= 0);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = __shfl_sync(0xffffffffu, code, 4 * i + (lane >> 3));
+    st[4 + i] = ldg_stream(hi + (long long)c * kHi + 8 * (lane & 7), c >= 0);
+  }
+}
+// 16 codes times the scale byte's power of two, as 16 bf16 values.
+__device__ __forceinline__ void codes_to_bf16(const uint4& v, uint32_t scale_byte, uint4& lo, uint4& hi) {
   const float s = scale_value(scale_byte);
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t o[8];
@@ -244,38 +271,41 @@ __device__ __forceinline__ void store_codes(uint8_t* sKV, int row, int cb, int c
   for (int i = 0; i < 4; ++i) {
     float f[4];
     e4m3x4_scaled(w[i], s, f);
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(f[0], f[1]), hi = __floats2bfloat162_rn(f[2], f[3]);
-    o[2 * i] = *reinterpret_cast<const uint32_t*>(&lo);
-    o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&hi);
+    const __nv_bfloat162 x = __floats2bfloat162_rn(f[0], f[1]), y = __floats2bfloat162_rn(f[2], f[3]);
+    o[2 * i] = *reinterpret_cast<const uint32_t*>(&x);
+    o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&y);
   }
-  sts16(tile_at(sKV, row, cb, cc), o[0], o[1], o[2], o[3]);
-  sts16(tile_at(sKV, row, cb, cc + 1), o[4], o[5], o[6], o[7]);
+  lo = make_uint4(o[0], o[1], o[2], o[3]);
+  hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
-__device__ __forceinline__ void store_fp8(const uint4 (&st)[24], const uint2& sc, int mb,
-                                          uint8_t* sKV, int hf, int row0, int lane) {
+// Four 16-code chunks of a pair (half 0 or 1 of the thread's eight; pair 3 has only half 0)
+// as bf16, and their store.
+__device__ __forceinline__ void convert_fp8(const uint4 (&st)[kStage], const uint2& sc, int mb, int half,
+                                            uint4 (&cv)[8], int lane) {
   const uint32_t word = mb < 2 ? sc.x : sc.y;   // scales of groups 4 (mb / 2) .. + 3
-  if (mb < 3) {
-    const int ch = (lane & 3) + ((lane >> 1) & 4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 4 * i + ((lane >> 2) & 1) + ((lane >> 3) & 2);
-      const uint32_t w = __shfl_sync(0xffffffffu, word, 16 * hf + r);
-      store_codes(sKV, row0 + r, 2 * mb + (ch >> 2), 2 * (ch & 3), st[4 * mb + i],
-                  (w >> (16 * (mb & 1) + 8 * (ch >> 2))) & 0xffu);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = 8 * i + (lane >> 2);
-      const uint32_t w = __shfl_sync(0xffffffffu, word, 16 * hf + r);
-      store_codes(sKV, row0 + r, 6, 2 * (lane & 3), st[12 + i], (w >> 16) & 0xffu);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 v = st[14 + i];
-      sts16(tile_at(sKV, row0 + 4 * i + (lane >> 3), 7, lane & 7), v.x, v.y, v.z, v.w);
-    }
+  for (int i = 0; i < 4; ++i) {
+    const int x = 4 * half + i;
+    const uint32_t w = __shfl_sync(0xffffffffu, word, mb < 3 ? fp8_row(x, lane) : 8 * x + (lane >> 2));
+    const int shift = mb < 3 ? 16 * (mb & 1) + 8 * (fp8_chunk(lane) >> 2) : 16;
+    codes_to_bf16(st[mb < 3 ? 8 * mb + x : x], (w >> shift) & 0xffu, cv[2 * i], cv[2 * i + 1]);
   }
+}
+__device__ __forceinline__ void sts16(uint8_t* d, const uint4& v) { sts16(d, v.x, v.y, v.z, v.w); }
+__device__ __forceinline__ void store_fp8(const uint4 (&cv)[8], int mb, int half, uint8_t* sKV, int row0,
+                                          int lane) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int x = 4 * half + i;
+    const int r = row0 + (mb < 3 ? fp8_row(x, lane) : 8 * x + (lane >> 2));
+    const int ch = mb < 3 ? fp8_chunk(lane) : lane & 3;
+    sts16(tile_at(sKV, r, 2 * mb + (ch >> 2), 2 * (ch & 3)), cv[2 * i]);
+    sts16(tile_at(sKV, r, 2 * mb + (ch >> 2), 2 * (ch & 3) + 1), cv[2 * i + 1]);
+  }
+}
+__device__ __forceinline__ void store_hi(const uint4 (&st)[kStage], uint8_t* sKV, int row0, int lane) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sts16(tile_at(sKV, row0 + 4 * i + (lane >> 3), 7, lane & 7), st[4 + i]);
 }
 
 // This thread's part of a pair is in shared memory: publish it to the tensor core and arrive
@@ -283,14 +313,13 @@ __device__ __forceinline__ void store_fp8(const uint4 (&st)[24], const uint2& sc
 __device__ __forceinline__ void pair_landed(int mb) {
   tc::fence_proxy_async();
   tc::tc_fence_before();
-  tc::named_bar_arrive(4 + mb, kThr);
+  tc::named_bar_arrive(4 + mb, kBarP);
 }
 
-// The query heads of a token into shared memory (cp.async; eight warps, eight heads each).
+// The query heads of a token into shared memory (cp.async, by the producer warps).
 __device__ __forceinline__ void load_q(const ChunkTc& p, int tok, uint8_t* sQ, int warp, int lane) {
   const __nv_bfloat16* qb = p.q + (long long)tok * kH * kD;
-  tc::cp_async_wait_all();   // queries fetched for an item that turned out empty
-  for (int h = warp; h < kH; h += kSW) {
+  for (int h = warp; h < kH; h += kPW) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int c = lane + 32 * x;
@@ -308,7 +337,8 @@ __device__ __forceinline__ float rel_weight(float x, float top) {
 }
 
 template <bool FP8>
-__global__ void __launch_bounds__(kLaunch, 1) chunk_tc_kernel(ChunkTc p) {
+__global__ void __launch_bounds__(kLaunch, 1)
+    chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ ChunkTc p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* sKV = base;                            // 8 x 16 KB
@@ -319,11 +349,14 @@ __global__ void __launch_bounds__(kLaunch, 1) chunk_tc_kernel(ChunkTc p) {
   float* s_Mu = s_M + kH;                         // the same, 0 where it is -inf
   float* s_alpha = s_Mu + kH;
   float* s_sink2 = s_alpha + kH;
-  int* s_flag = reinterpret_cast<int*>(s_sink2 + kH);
+  float* s_zero = s_sink2 + kH;
+  int* s_flag = reinterpret_cast<int*>(s_zero + kH);
   uint64_t* bar_s = reinterpret_cast<uint64_t*>(s_flag + 4);
   uint64_t* bar_pv = bar_s + 1;                   // [4]
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bar_pv + 4);
-  int32_t* s_cu = reinterpret_cast<int32_t*>(tmem_holder + 2);   // [kSeqCache + 1]
+  uint64_t* bar_full = bar_pv + 4;                // [4]: a pair's TMA copies have landed
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bar_full + 4);
+  uint32_t* s_valid = tmem_holder + 2;            // [4] the tile's rows that exist, a bit each
+  int32_t* s_cu = reinterpret_cast<int32_t*>(s_valid + 4);   // [kSeqCache + 1]
   int32_t* s_pos0 = s_cu + kSeqCache + 1;         // [kSeqCache]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -335,10 +368,10 @@ __global__ void __launch_bounds__(kLaunch, 1) chunk_tc_kernel(ChunkTc p) {
   }
   const int32_t* cu = cached ? s_cu : p.cu_q;
   const int32_t* pos0 = cached ? s_pos0 : p.pos0;
-  if (tid < kH) s_sink2[tid] = p.sink[tid] * kLog2e;
+  if (tid < kH) { s_sink2[tid] = p.sink[tid] * kLog2e; s_zero[tid] = 0.f; }
   if (tid == 0) {
     tc::mbar_init(bar_s, 1);
-    for (int i = 0; i < 4; ++i) tc::mbar_init(bar_pv + i, 1);
+    for (int i = 0; i < 8; ++i) tc::mbar_init(bar_pv + i, 1);
     tc::fence_barrier_init();
   }
   if (warp == 0) tc::tmem_alloc(tmem_holder, 512);
@@ -348,172 +381,222 @@ __global__ void __launch_bounds__(kLaunch, 1) chunk_tc_kernel(ChunkTc p) {
   const uint32_t tmem = *tmem_holder;
   const uint32_t tS = tmem, tO = tmem + 64;       // columns [0, 64) S^T; [64, 320) O^T
 
-  if (warp >= kSW) {
+  if (warp >= kSW + kPW) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
     // ------------------------------------------------------------------ MMA issuer
-    if (warp == kSW) {
+    if (warp == kSW + kPW) {
     constexpr uint32_t idS = tc::instr_desc(128, kH, 1, 1, 0, 0);   // K-major x K-major
     constexpr uint32_t idO = tc::instr_desc(128, kH, 1, 1, 1, 1);   // MN-major x MN-major
     const uint64_t dS_a = tc::smem_desc_sw128(tc::smem_u32(sKV), 16, 1024);
     const uint64_t dS_b = tc::smem_desc_sw128(tc::smem_u32(sQ), 16, 1024);
     const uint64_t dO_a = tc::smem_desc_sw128(tc::smem_u32(sKV), kKVBlk, 1024);
     const uint64_t dO_b = tc::smem_desc_sw128(tc::smem_u32(sP), 8192, 1024);
+    const uint32_t uS = __shfl_sync(0xffffffffu, tS, 0), uO = uS + 64;
+    const uint32_t el = tc::elect_one();
     for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
       const Item I = get_item(p, cu, pos0, item, lane);
       if (!I.live) break;
       for (int j = I.tb; j < I.te; ++j) {
+#pragma unroll
         for (int mb = 0; mb < 4; ++mb) {
-          tc::named_bar(4 + mb, kThr);             // the pair (and, with the first, q) is in place
-          if (lane == 0) {
-            tc::tc_fence_after();
-#pragma unroll
-            for (int kb = 2 * mb; kb < 2 * mb + 2; ++kb) {
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                tc::mma_f16(tS, tc::desc_advance(dS_a, kb * kKVBlk + kk * 32),
-                            tc::desc_advance(dS_b, kb * kQBlk + kk * 32), idS, (kb | kk) != 0);
-            }
-            if (mb == 3) tc::mma_commit(bar_s);
-          }
-          __syncwarp();
-        }
-        tc::named_bar(2, kThr);                    // P^T in place, O^T rescaled
-        if (lane == 0) {
+          tc::named_bar(4 + mb, kBarP);             // the pair (and, with the first, q) is in place
           tc::tc_fence_after();
 #pragma unroll
-          for (int mb = 0; mb < 4; ++mb) {
+          for (int kb = 2 * mb; kb < 2 * mb + 2; ++kb) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              tc::mma_f16(tO + mb * kH, tc::desc_advance(dO_a, 2 * mb * kKVBlk + kk * 2048),
-                          tc::desc_advance(dO_b, kk * 2048), idO, (j > I.tb) || (kk > 0));
-            tc::mma_commit(bar_pv + mb);           // column blocks 2 mb, 2 mb + 1 are free
+            for (int kk = 0; kk < 4; ++kk)
+              tc::mma_f16_el(uS, tc::desc_advance(dS_a, kb * kKVBlk + kk * 32),
+                             tc::desc_advance(dS_b, kb * kQBlk + kk * 32), idS, (kb | kk) != 0, el);
           }
         }
+        if (el) tc::mma_commit(bar_s);
         __syncwarp();
+        tc::named_bar(2, kBarS);                    // P^T in place, O^T rescaled
+        tc::tc_fence_after();
+#pragma unroll
+        for (int mb = 0; mb < 4; ++mb) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc::mma_f16_el(uO + mb * kH, tc::desc_advance(dO_a, 2 * mb * kKVBlk + kk * 2048),
+                           tc::desc_advance(dO_b, kk * 2048), idO, (kk > 0) || (j > I.tb), el);
+          if (el) tc::mma_commit(bar_pv + mb);     // column blocks 2 mb, 2 mb + 1 are free
+          __syncwarp();
+        }
       }
     }
     }
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    // ------------------------------------------------------------------ gather and softmax
-    const int qd = warp & 3, hf = warp >> 2;
-    const int row = qd * 32 + lane;                // TMEM lane = tile row of this thread
-    const int row0 = qd * 32 + 16 * hf;            // first of the 16 rows this warp moves
-    const uint32_t lane_addr = (uint32_t)(qd * 32) << 16;
-    uint32_t ns = 0, npv = 0;                      // phases of bar_s and bar_pv waited for
-    bool ok = true, pv_pending = false;
-    int q_item = -1;                               // item whose queries are in sQ or on their way
-
-    uint4 st[24];
+  } else if (warp >= kSW) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsProd));
+    // ------------------------------------------------------------------ producers
+    const int qd = warp - kSW;                     // this warp's quarter of a tile's rows
+    const int row0 = qd * 32;
+    bool ok = true;
+    uint4 st[kStage];
     uint2 sc = make_uint2(0u, 0u);
+    uint64_t src = 0;
     Stream S;
     S.item = blockIdx.x;
     S.live = S.item < p.items;
-    S.it.te = 0; S.tile = 0;
+    S.it.te = S.tile = 0;
     if (S.live) {
       S.it = get_item(p, cu, pos0, S.item, lane);
       S.live = S.it.live;
       S.tile = S.it.tb;
-      if (S.live && S.it.te > S.it.tb) {
-        load_q(p, S.it.tok, sQ, warp, lane);
-        q_item = S.item;
-      }
       stream_settle(S, p, cu, pos0, lane);
     }
-    // the first tile's rows and loads, then the second tile's list entries and pages
+    // the first tile's row numbers, loads and queries, then the second tile's rows
     RowRef nx;
-    row_entry(nx, S, p, row);
+    row_entry(nx, S, p, qd * 32 + lane);
     row_page(nx, S.it.seq, p);
-    int code = row_code(nx, p);
-    bool window = nx.window;
-    auto issue = [&]() {
+    int code = -1;
+    bool window = false, whole = false, live = false, new_q = false;
+    uint32_t have = 0;                             // rows of the quarter that exist
+    int item = -1;
+    auto take = [&]() {   // nx becomes the staged tile; its loads go out; nx is the next one's entries
+      live = S.live;
+      if (!live) return;
+      code = row_code(nx, p);
+      window = nx.window;
+      new_q = S.item != item;
+      item = S.item;
+      have = __ballot_sync(0xffffffffu, code >= 0);
+      // 128 consecutive rows of one page that all exist come by TMA, straight into the tile
+      whole = !FP8 && !window && !p.idx && (S.tile + 1) * kRows <= S.it.nsel && have == 0xffffffffu;
       if (FP8 && !window) {
-        load_fp8(st, sc, p, code, hf, lane);
-      } else {
-#pragma unroll
-        for (int mb = 0; mb < 3; ++mb) load_bf16(st, mb, mb, p, window, code, hf, lane);
+        load_fp8(st, sc, p, code, lane);
+      } else if (!whole) {
+        src = row_addr(p, window, code);
+        load_bf16(st, 0, 2, src, lane);
+      }
+      if (!new_q) {
+        ++S.tile;
+        stream_settle(S, p, cu, pos0, lane);
+        row_entry(nx, S, p, qd * 32 + lane);
       }
     };
-    if (S.live) {
-      issue();
+    auto queries = [&]() {   // the item's first tile: its queries too
+      if (!live || !new_q) return;
+      load_q(p, S.it.tok, sQ, qd, lane);
       ++S.tile;
       stream_settle(S, p, cu, pos0, lane);
-      row_entry(nx, S, p, row);
-      row_page(nx, S.it.seq, p);
+      row_entry(nx, S, p, qd * 32 + lane);
+    };
+    take();
+    queries();
+    uint32_t n_tma = 0;                            // tiles brought by TMA
+    for (uint32_t n = 0; live; ++n) {
+      const bool wait_q = new_q;
+      if (!FP8 && whole) {
+#pragma unroll
+        for (int mb = 0; mb < 4; ++mb) {
+          if (n > 0) {
+            ok = ok && tc::mbar_wait_hint(bar_pv + mb, (n - 1) & 1, p.err, kHintNs);
+            tc::tc_fence_after();
+          }
+          if (qd == 0 && lane == 0) {              // lane 0 of quarter 0: the tile's first row
+            tc::mbar_arrive_expect_tx(bar_full + mb, 2 * kKVBlk);
+            tc::tma_load_2d(sKV + 2 * mb * kKVBlk, &tm_rows, 128 * mb, code, bar_full + mb);
+            tc::tma_load_2d(sKV + (2 * mb + 1) * kKVBlk, &tm_rows, 128 * mb + 64, code, bar_full + mb);
+          }
+        }
+        row_page(nx, S.it.seq, p);
+        if (lane == 0) s_valid[qd] = have;
+        if (wait_q) tc::cp_async_wait_all();
+#pragma unroll
+        for (int mb = 0; mb < 4; ++mb) {
+          ok = ok && tc::mbar_wait_hint(bar_full + mb, n_tma & 1, p.err, kHintNs);
+          pair_landed(mb);
+        }
+        ++n_tma;
+      } else {
+#pragma unroll
+        for (int mb = 0; mb < 4; ++mb) {
+          const bool fp8 = FP8 && !window;
+          uint4 cv[8];
+          if (fp8) convert_fp8(st, sc, mb, 0, cv, lane);
+          if (n > 0) {
+            ok = ok && tc::mbar_wait_hint(bar_pv + mb, (n - 1) & 1, p.err, kHintNs);
+            tc::tc_fence_after();
+          }
+          if (fp8) {
+            store_fp8(cv, mb, 0, sKV, row0, lane);
+            if (mb < 3) {
+              convert_fp8(st, sc, mb, 1, cv, lane);
+              store_fp8(cv, mb, 1, sKV, row0, lane);
+            } else {
+              store_hi(st, sKV, row0, lane);
+            }
+          } else {
+            store_bf16(st, mb, sKV, row0, lane);
+          }
+          if (mb == 0) {
+            if (lane == 0) s_valid[qd] = have;
+            if (wait_q) tc::cp_async_wait_all();
+          }
+          pair_landed(mb);
+          if (!fp8 && mb < 2) load_bf16(st, mb + 2, 1, src, lane);
+          if (fp8 && mb == 1) load_fp8_last(st, p, code, lane);
+          if (mb == 2) row_page(nx, S.it.seq, p);
+        }
+      }
+      take();
+      if (live && new_q) {
+        // the queries in shared memory are read by this tile's S^T for the last time
+        ok = ok && tc::mbar_wait_hint(bar_s, n & 1, p.err, kHintNs);
+        tc::tc_fence_after();
+        queries();
+      }
     }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    // ------------------------------------------------------------------ softmax and output
+    const int qd = warp & 3, hf = warp >> 2;
+    const int row = qd * 32 + lane;                // TMEM lane = tile row of this thread
+    const uint32_t lane_addr = (uint32_t)(qd * 32) << 16;
+    uint32_t ns = 0;                               // tiles so far
+    bool ok = true;
 
     for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
       const Item I = get_item(p, cu, pos0, item, lane);
       if (!I.live) break;
+      bool started = false;                        // a tile of this item had a row
       float lsum[32];
 #pragma unroll
       for (int h = 0; h < 32; ++h) lsum[h] = 0.f;
-      if (I.te > I.tb && q_item != item) {
-        load_q(p, I.tok, sQ, warp, lane);
-        q_item = item;
-      }
       for (int j = I.tb; j < I.te; ++j) {
-        // the staged tile into shared memory, pair by pair as the previous PV frees the pairs
-#pragma unroll
-        for (int mb = 0; mb < 4; ++mb) {
-          if (pv_pending) {
-            ok = ok && tc::mbar_wait_hint(bar_pv + mb, npv & 1, p.err, kHintNs);
-            tc::tc_fence_after();
-          }
-          if (FP8 && !window) store_fp8(st, sc, mb, sKV, hf, row0, lane);
-          else store_bf16(st, mb == 3 ? 0 : mb, mb, sKV, row0, lane);
-          if (mb == 0) {
-            if (!(FP8 && !window)) load_bf16(st, 0, 3, p, window, code, hf, lane);
-            if (j == I.tb) tc::cp_async_wait_all();   // the queries
-          }
-          pair_landed(mb);
-        }
-        if (pv_pending) ++npv;
-        const bool valid = code >= 0;
-        const bool last = j == I.te - 1;
-        // the next tile's loads, and the list entries of the one after it
-        const bool more = S.live;
-        if (more) {
-          code = row_code(nx, p);
-          window = nx.window;
-          issue();
-          ++S.tile;
-          stream_settle(S, p, cu, pos0, lane);
-          row_entry(nx, S, p, row);
-        }
-
         ok = ok && tc::mbar_wait_hint(bar_s, ns & 1, p.err, kHintNs);
         ++ns;
         tc::tc_fence_after();
-        if (last && item + (int)gridDim.x < p.items) {
-          // S^T was the last reader of these queries: fetch the next item's
-          const int tok = (item + (int)gridDim.x) / p.nsplit;
-          if (tok < cu[p.b]) {
-            load_q(p, tok, sQ, warp, lane);
-            q_item = item + (int)gridDim.x;
-          }
-        }
-        uint32_t lg[32];                           // logits (float bits), log2 units
-        auto logits = [&]() {
+        const uint32_t have = s_valid[qd];
+        const bool valid = (have >> lane) & 1u;
+        const bool full = have == 0xffffffffu;
+        // logits less the running maximum, log2 units
+        uint32_t lg[32];
+        auto logits = [&](const float* ref) {
           tc::tmem_ld32(tS + lane_addr + 32 * hf, lg);
           tc::tmem_ld_wait(lg);
 #pragma unroll
-          for (int h = 0; h < 32; ++h)
-            lg[h] = __float_as_uint(valid ? __uint_as_float(lg[h]) * p.scale_log2 : -INFINITY);
-        };
-        logits();
-        bool exact = j == I.tb;
-        if (!exact) {
-          bool big = false;
-#pragma unroll
           for (int h = 0; h < 32; h += 4) {
-            const float4 M4 = *reinterpret_cast<const float4*>(s_M + 32 * hf + h);
-            big |= __uint_as_float(lg[h]) > M4.x + kRescale;
-            big |= __uint_as_float(lg[h + 1]) > M4.y + kRescale;
-            big |= __uint_as_float(lg[h + 2]) > M4.z + kRescale;
-            big |= __uint_as_float(lg[h + 3]) > M4.w + kRescale;
+            const float4 M4 = *reinterpret_cast<const float4*>(ref + 32 * hf + h);
+            lg[h] = __float_as_uint(fmaf(__uint_as_float(lg[h]), p.scale_log2, -M4.x));
+            lg[h + 1] = __float_as_uint(fmaf(__uint_as_float(lg[h + 1]), p.scale_log2, -M4.y));
+            lg[h + 2] = __float_as_uint(fmaf(__uint_as_float(lg[h + 2]), p.scale_log2, -M4.z));
+            lg[h + 3] = __float_as_uint(fmaf(__uint_as_float(lg[h + 3]), p.scale_log2, -M4.w));
           }
-          exact = tc::bar_red_or(3, kST, big);
+          if (!full) {
+#pragma unroll
+            for (int h = 0; h < 32; ++h)
+              if (!valid) lg[h] = __float_as_uint(-INFINITY);
+          }
+        };
+        // the item's first tile, and any up to the first with a row, set the maximum
+        bool exact = !started;
+        logits(exact ? s_zero : s_Mu);
+        if (!exact) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int h = 0; h < 32; ++h) top = fmaxf(top, __uint_as_float(lg[h]));
+          exact = tc::bar_red_or(3, kST, top > kRescale);
         }
         if (exact) {
           // the reduction consumes the logits, which are read from TMEM again below (keeping
@@ -528,14 +611,16 @@ __global__ void __launch_bounds__(kLaunch, 1) chunk_tc_kernel(ChunkTc p) {
           }
           tc::named_bar(3, kST);
           if (tid < kH) {
+            // this tile's maxima, relative to the reference that the logits were taken against
             const float tm = fmaxf(fmaxf(s_red[tid], s_red[kH + tid]), fmaxf(s_red[2 * kH + tid], s_red[3 * kH + tid]));
             const float Mr = s_M[tid];
             float Mn = Mr, al = 1.f;
-            if (j == I.tb) {
+            if (!started) {
               Mn = tm;
-            } else if (tm > Mr + kRescale) {
-              Mn = tm;
-              al = exp2f(Mr - tm);
+              al = 0.f;                            // O^T, if any, is zero so far
+            } else if (tm > kRescale) {
+              Mn = Mr + tm;
+              al = exp2f(-tm);
               s_flag[0] = 1;
             }
             s_M[tid] = Mn;
@@ -543,7 +628,7 @@ __global__ void __launch_bounds__(kLaunch, 1) chunk_tc_kernel(ChunkTc p) {
             s_alpha[tid] = al;
           }
           tc::named_bar(3, kST);
-          if (j > I.tb && s_flag[0]) {
+          if (started && s_flag[0]) {
             for (int mb = 2 * hf; mb < 2 * hf + 2; ++mb) {
 #pragma unroll
               for (int half = 0; half < 2; ++half) {
@@ -561,7 +646,8 @@ __global__ void __launch_bounds__(kLaunch, 1) chunk_tc_kernel(ChunkTc p) {
 #pragma unroll
             for (int h = 0; h < 32; ++h) lsum[h] *= s_alpha[32 * hf + h];
           }
-          logits();
+          started = s_M[0] != -INFINITY;           // rows are masked for all heads alike
+          logits(s_Mu);
         }
         // probabilities: bf16 into P^T (this row's 128-byte line, four 16-byte chunks of it);
         // the sums take them before that rounding
@@ -569,23 +655,19 @@ __global__ void __launch_bounds__(kLaunch, 1) chunk_tc_kernel(ChunkTc p) {
         for (int cb = 0; cb < 4; ++cb) {
           uint32_t w4[4];
 #pragma unroll
-          for (int e = 0; e < 4; e += 2) {
+          for (int e = 0; e < 4; ++e) {
             const int h = cb * 8 + 2 * e;
-            const float4 M4 = *reinterpret_cast<const float4*>(s_Mu + 32 * hf + h);
-            const float p0 = exp2f(__uint_as_float(lg[h]) - M4.x), p1 = exp2f(__uint_as_float(lg[h + 1]) - M4.y);
-            const float p2 = exp2f(__uint_as_float(lg[h + 2]) - M4.z), p3 = exp2f(__uint_as_float(lg[h + 3]) - M4.w);
-            lsum[h] += p0; lsum[h + 1] += p1; lsum[h + 2] += p2; lsum[h + 3] += p3;
-            const __nv_bfloat162 a = __floats2bfloat162_rn(p0, p1), b2 = __floats2bfloat162_rn(p2, p3);
+            const float p0 = ex2(__uint_as_float(lg[h])), p1 = ex2(__uint_as_float(lg[h + 1]));
+            lsum[h] += p0;
+            lsum[h + 1] += p1;
+            const __nv_bfloat162 a = __floats2bfloat162_rn(p0, p1);
             w4[e] = *reinterpret_cast<const uint32_t*>(&a);
-            w4[e + 1] = *reinterpret_cast<const uint32_t*>(&b2);
           }
           sts16(sP + row * 128 + (((4 * hf + cb) ^ (row & 7)) << 4), w4[0], w4[1], w4[2], w4[3]);
         }
         tc::fence_proxy_async();
         tc::tc_fence_before();
-        tc::named_bar_arrive(2, kThr);
-        pv_pending = true;
-        if (more) row_page(nx, S.it.seq, p);
+        tc::named_bar_arrive(2, kBarS);
       }
 
       // ---------------------------------------------------------------- the item's output
@@ -623,7 +705,7 @@ __global__ void __launch_bounds__(kLaunch, 1) chunk_tc_kernel(ChunkTc p) {
       tc::named_bar(3, kST);
       if (p.nsplit > 1) {
         for (int mb = 2 * hf; mb < 2 * hf + 2; ++mb) {
-          ok = ok && tc::mbar_wait_hint(bar_pv + mb, npv & 1, p.err, kHintNs);
+          ok = ok && tc::mbar_wait_hint(bar_pv + mb, (ns - 1) & 1, p.err, kHintNs);
           tc::tc_fence_after();
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
@@ -638,12 +720,9 @@ __global__ void __launch_bounds__(kLaunch, 1) chunk_tc_kernel(ChunkTc p) {
                            : make_float4(nan_f(), nan_f(), nan_f(), nan_f());
           }
         }
-        // the pairs this half did not wait for: the next tile may overwrite all four
-        for (int mb = 2 - 2 * hf; mb < 4 - 2 * hf; ++mb)
-          ok = ok && tc::mbar_wait_hint(bar_pv + mb, npv & 1, p.err, kHintNs);
       } else {
         for (int mb = 0; mb < 4; ++mb) {
-          ok = ok && tc::mbar_wait_hint(bar_pv + mb, npv & 1, p.err, kHintNs);
+          ok = ok && tc::mbar_wait_hint(bar_pv + mb, (ns - 1) & 1, p.err, kHintNs);
           tc::tc_fence_after();
           uint32_t o[32];
           tc::tmem_ld32(tO + mb * kH + 32 * hf + lane_addr, o);
@@ -673,8 +752,6 @@ __global__ void __launch_bounds__(kLaunch, 1) chunk_tc_kernel(ChunkTc p) {
           }
         }
       }
-      ++npv;
-      pv_pending = false;
       tc::tc_fence_before();
       tc::named_bar(3, kST);                       // s_red, s_alpha and s_M are free again
     }
@@ -742,7 +819,7 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(ChunkTc p) {
   *reinterpret_cast<uint2*>(p.out + ((long long)tok * kH + h) * kD + d) = v;
 }
 
-constexpr size_t kSmem = 1024 + 8 * kKVBlk + 8 * kQBlk + kRows * 128 + (4 * kH + 4 * kH) * 4 + 16 + 5 * 8 + 8 +
+constexpr size_t kSmem = 1024 + 8 * kKVBlk + 8 * kQBlk + kRows * 128 + (4 * kH + 5 * kH) * 4 + 16 + 9 * 8 + 8 + 16 +
                          (2 * kSeqCache + 1) * 4;
 static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 
@@ -817,8 +894,13 @@ csa_status launch_chunk_attn_tc(const ChunkArgs& a, const csa_kv_cache& kv, void
   auto kern = kv.dtype == CSA_FP8_E4M3 ? chunk_tc_kernel<true> : chunk_tc_kernel<false>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
     return CSA_ERR_CUDA;
+  // bf16 pages as one matrix of rows, copied in column blocks of 64 dims of a tile's 128 rows
+  CUtensorMap tm{};
+  if (kv.dtype == CSA_BF16 &&
+      !make_tmap_2d_b16(&tm, kv.rows, kD, (uint64_t)kv.num_pages * kPageEntries, 64, kRows))
+    return CSA_ERR_CUDA;
   const int grid = (int)std::min<long long>(items, sm_count());
-  if (csa_launch(kern, dim3(grid), dim3(kLaunch), kSmem, st, false, p) != cudaSuccess) return CSA_ERR_CUDA;
+  if (csa_launch(kern, dim3(grid), dim3(kLaunch), kSmem, st, false, tm, p) != cudaSuccess) return CSA_ERR_CUDA;
   if (p.nsplit > 1 &&
       csa_launch(chunk_merge_kernel, dim3(a.N, kD / kMergeDims), dim3(256), 0, st, true, p) != cudaSuccess)
     return CSA_ERR_CUDA;
