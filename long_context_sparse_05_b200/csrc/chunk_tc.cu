@@ -64,7 +64,7 @@ constexpr int kBarS = kST + 32;       // threads of a barrier of the softmax and
 constexpr int kBarP = 32 * kPW + 32;  // ... of the producers and the MMA warp
 constexpr int kLaunch = 512;
 // Registers a thread by warpgroup (2 x softmax, producers, MMA), out of 4 x 128 at launch.
-constexpr int kRegsSoftmax = 112, kRegsProd = 208, kRegsMma = 80;
+constexpr int kRegsSoftmax = 120, kRegsProd = 232, kRegsMma = 40;
 constexpr int kRegsLaunch = 128;      // 65,536 / 512
 // .dec must not raise a warpgroup's count and .inc must not lower it (either faults), and the
 // shares must fit what the block was launched with (or .inc waits for good).
@@ -171,16 +171,16 @@ __device__ __forceinline__ int row_code(const RowRef& r, const ChunkTc& p) {
   return (unsigned)r.pg < (unsigned)p.kv.num_pages ? r.pg * kPageEntries + r.e % kPageEntries : -1;
 }
 
-// 16 bytes of read-only data that nothing in this CTA reads again; zeros where !have.
-__device__ __forceinline__ uint4 ldg_stream(const void* p, bool have) {
+// 16 bytes of read-only data that nothing in this CTA reads again.
+__device__ __forceinline__ uint4 ldg_stream(const void* p) {
   uint4 v;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
-      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-      "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"((uint32_t)have));
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
+// What a row that does not exist is read from (a predicate on each load costs more than a
+// pointer chosen once per row).
+__device__ __align__(128) const uint8_t g_zero_row[kD * 2] = {};
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -196,32 +196,42 @@ __device__ __forceinline__ uint8_t* tile_at(uint8_t* sKV, int row, int cb, int c
 
 constexpr int kStage = 32;   // 16-byte registers a producer thread stages of the next tile
 
-// bf16 rows: producer warp qd moves rows 32 qd ..+31 of the tile; lane = (row parity, 16-byte
-// chunk of a 128-dim pair).  `src` is the address of this lane's row of the quarter (0: none).
-// Two of the four pairs are staged; the other two are loaded into their registers as those
-// are stored.
-__device__ __forceinline__ void load_bf16(uint4 (&st)[kStage], int mb0, int nmb, uint64_t src, int lane) {
+// Producer warp qd moves rows 32 qd ..+31 of the tile; lane = (row of four, 16-byte chunk of
+// eight): rows 4 i + lane / 8, i < 8, 128 contiguous bytes of a row at a time (64-byte pieces
+// take twice the tag lookups: 1,200 instead of 600 cycles for a tile's 128 loads).  The rows'
+// places are shuffled to their lanes ahead of all loads: a shuffle between loads waits behind
+// them in the same queue.
+//
+// bf16 rows: two of a tile's four 128-dim pairs are staged; the other two are loaded into
+// their registers as those are stored.
+struct RowPtrs { const char* a[8]; };
+__device__ __forceinline__ void row_ptrs(RowPtrs& r, uint64_t src, int lane) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint64_t row = __shfl_sync(0xffffffffu, src, 2 * i + (lane >> 4));
-    const char* a = reinterpret_cast<const char*>(row) + 16 * (lane & 15);
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-      if (x < nmb) st[16 * ((mb0 + x) & 1) + i] = ldg_stream(a + 256 * (mb0 + x), row != 0);
+  for (int i = 0; i < 8; ++i) {
+    const uint64_t x = __shfl_sync(0xffffffffu, src, 4 * i + (lane >> 3));
+    r.a[i] = reinterpret_cast<const char*>(x) + 16 * (lane & 7);
   }
 }
+__device__ __forceinline__ void load_bf16(uint4 (&st)[kStage], int mb, const RowPtrs& r) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) st[16 * (mb & 1) + 2 * i + j] = ldg_stream(r.a[i] + 256 * mb + 128 * j);
+  }
+}
+__device__ __forceinline__ void sts16(uint8_t* d, const uint4& v) { sts16(d, v.x, v.y, v.z, v.w); }
 __device__ __forceinline__ void store_bf16(const uint4 (&st)[kStage], int mb, uint8_t* sKV, int row0,
                                            int lane) {
-  const int c = 16 * mb + (lane & 15);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint4 v = st[16 * (mb & 1) + i];
-    sts16(tile_at(sKV, row0 + 2 * i + (lane >> 4), c >> 3, c & 7), v.x, v.y, v.z, v.w);
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      sts16(tile_at(sKV, row0 + 4 * i + (lane >> 3), 2 * mb + j, lane & 7), st[16 * (mb & 1) + 2 * i + j]);
   }
 }
 // Address of a plain row: in the pool, in new_win or in the rings.
 __device__ __forceinline__ uint64_t row_addr(const ChunkTc& p, bool window, int code) {
-  if (code < 0) return 0;
+  if (code < 0) return reinterpret_cast<uint64_t>(g_zero_row);
   const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(p.kv.rows);
   if (window) {
     base = code >= kNewTag ? p.new_win : p.win;
@@ -230,82 +240,115 @@ __device__ __forceinline__ uint64_t row_addr(const ChunkTc& p, bool window, int 
   return reinterpret_cast<uint64_t>(base + (long long)code * kD);
 }
 
-// FP8 rows: pairs 0-2 are staged, lane = (code chunk of 16 dims, row), the row in three bits
-// of the lane so that eight lanes store to 128 distinct bytes; pair 3 (the last 64 codes and
-// the 64 bf16 dims) is loaded into the registers of pairs 0 and 1 as those are stored.
-__device__ __forceinline__ int fp8_row(int i, int lane) { return 4 * i + ((lane >> 2) & 1) + ((lane >> 3) & 2); }
-__device__ __forceinline__ int fp8_chunk(int lane) { return (lane & 3) + ((lane >> 1) & 4); }
-__device__ __forceinline__ void load_fp8(uint4 (&st)[kStage], uint2& sc, const ChunkTc& p, int code, int lane) {
-  const uint8_t* rows = static_cast<const uint8_t*>(p.kv.rows);
-  sc = make_uint2(0u, 0u);
+// FP8 rows: pairs 0-2 are staged (a row's 128 codes of a pair are eight lanes' chunks); pair 3
+// (the last 64 codes and the 64 bf16 dims) is loaded into the registers of pairs 0 and 1 as
+// those are stored.  The scale words of the quarter's rows stay with their rows' lanes.
+__device__ __forceinline__ void load_fp8(uint4 (&st)[kStage], uint2& sc, int (&c)[8], const ChunkTc& p,
+                                         int code, int lane) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = __shfl_sync(0xffffffffu, code, 4 * i + (lane >> 3));
+  sc = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);       // a row that does not exist: zeros times 1
   if (code >= 0)
     sc = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.kv.scales) + (long long)code * 8));
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int c = __shfl_sync(0xffffffffu, code, fp8_row(i, lane));
-    const uint8_t* a = rows + (long long)c * kNc + 16 * fp8_chunk(lane);
+    const uint8_t* a = (c[i] >= 0 ? static_cast<const uint8_t*>(p.kv.rows) + (long long)c[i] * kNc : g_zero_row) +
+                       16 * (lane & 7);
 #pragma unroll
-    for (int mb = 0; mb < 3; ++mb) st[8 * mb + i] = ldg_stream(a + 128 * mb, c >= 0);
+    for (int mb = 0; mb < 3; ++mb) st[8 * mb + i] = ldg_stream(a + 128 * mb);
   }
 }
-__device__ __forceinline__ void load_fp8_last(uint4 (&st)[kStage], const ChunkTc& p, int code, int lane) {
-  const uint8_t* rows = static_cast<const uint8_t*>(p.kv.rows);
-  const __nv_bfloat16* hi = static_cast<const __nv_bfloat16*>(p.kv.hi);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = __shfl_sync(0xffffffffu, code, 8 * i + (lane >> 2));
-    st[i] = ldg_stream(rows + (long long)c * kNc + 384 + 16 * (lane & 3), c >= 0);
-  }
+// Pair 3: lanes 0-3 of eight take the row's codes, and all eight its bf16 dims.
+__device__ __forceinline__ void load_fp8_last(uint4 (&st)[kStage], const int (&c)[8], const ChunkTc& p,
+                                              int lane) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int c = __shfl_sync(0xffffffffu, code, 4 * i + (lane >> 3));
-    st[4 + i] = ldg_stream(hi + (long long)c * kHi + 8 * (lane & 7), c >= 0);
+    const uint8_t* h = c[i] >= 0 ? reinterpret_cast<const uint8_t*>(static_cast<const __nv_bfloat16*>(p.kv.hi) +
+                                                                    (long long)c[i] * kHi)
+                                 : g_zero_row;
+    st[8 + i] = ldg_stream(h + 16 * (lane & 7));
   }
-}
-// 16 codes times the scale byte's power of two, as 16 bf16 values.
-__device__ __forceinline__ void codes_to_bf16(const uint4& v, uint32_t scale_byte, uint4& lo, uint4& hi) {
-  const float s = scale_value(scale_byte);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t o[8];
+  // codes: lane = (row of eight, chunk of four), so rows 8 i + lane / 4
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float f[4];
-    e4m3x4_scaled(w[i], s, f);
-    const __nv_bfloat162 x = __floats2bfloat162_rn(f[0], f[1]), y = __floats2bfloat162_rn(f[2], f[3]);
-    o[2 * i] = *reinterpret_cast<const uint32_t*>(&x);
-    o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&y);
+    const int x = __shfl_sync(0xffffffffu, c[2 * i], ((lane >> 2) & 3) * 8);
+    const int y = __shfl_sync(0xffffffffu, c[2 * i + 1], ((lane >> 2) & 3) * 8);
+    const int r = lane & 16 ? y : x;
+    st[i] = ldg_stream((r >= 0 ? static_cast<const uint8_t*>(p.kv.rows) + (long long)r * kNc + 384 : g_zero_row) +
+                       16 * (lane & 3));
   }
-  lo = make_uint4(o[0], o[1], o[2], o[3]);
-  hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
-// Four 16-code chunks of a pair (half 0 or 1 of the thread's eight; pair 3 has only half 0)
-// as bf16, and their store.
-__device__ __forceinline__ void convert_fp8(const uint4 (&st)[kStage], const uint2& sc, int mb, int half,
-                                            uint4 (&cv)[8], int lane) {
-  const uint32_t word = mb < 2 ? sc.x : sc.y;   // scales of groups 4 (mb / 2) .. + 3
+// Four codes times 2^k as four bf16 values, exactly.  Fast: two codes to f16 in one conversion,
+// one mixed-precision product each (f16 x f16 -> f32, the scale as an f16: `s` holds 2^k in
+// both halves), two to a bf16 pair: 222 cycles for a lane's 64 codes, against 329 through
+// float conversions and products (and 319 building the bf16 bits with integer operations).
+__device__ __forceinline__ uint2 codes_fast(uint32_t w, uint32_t s) {
+  uint32_t a, b;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}" : "=r"(a), "=r"(b) : "r"(w));
+  uint2 o;
+#define CSA_PAIR(dst, src)                                                                        \
+  asm("{\n\t.reg .b16 l, h, x;\n\t.reg .f32 f, g;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 {x, _}, %2;\n\t" \
+      "fma.rn.f32.f16 f, l, x, 0f80000000;\n\tfma.rn.f32.f16 g, h, x, 0f80000000;\n\t"             \
+      "cvt.rn.bf16x2.f32 %0, g, f;\n\t}" : "=r"(dst) : "r"(src), "r"(s))
+  CSA_PAIR(o.x, a);
+  CSA_PAIR(o.y, b);
+#undef CSA_PAIR
+  return o;
+}
+// The same for any scale.
+__device__ __forceinline__ uint2 codes_slow(uint32_t w, uint32_t scale_byte) {
+  float f[4];
+  e4m3x4_scaled(w, scale_value(scale_byte), f);
+  const __nv_bfloat162 x = __floats2bfloat162_rn(f[0], f[1]), y = __floats2bfloat162_rn(f[2], f[3]);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+}
+// Whether a row's seven scale bytes are all normal f16 powers of two (k in [-14, 15]: maxima of
+// a group between 0.03 and 1.4e7).
+__device__ __forceinline__ bool scales_fast(const uint2& sc) {
+  bool ok = true;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int x = 4 * half + i;
-    const uint32_t w = __shfl_sync(0xffffffffu, word, mb < 3 ? fp8_row(x, lane) : 8 * x + (lane >> 2));
-    const int shift = mb < 3 ? 16 * (mb & 1) + 8 * (fp8_chunk(lane) >> 2) : 16;
-    codes_to_bf16(st[mb < 3 ? 8 * mb + x : x], (w >> shift) & 0xffu, cv[2 * i], cv[2 * i + 1]);
+  for (int g = 0; g < 7; ++g) ok &= (((g < 4 ? sc.x : sc.y) >> (8 * (g & 3))) & 0xffu) - 113u <= 142u - 113u;
+  return ok;
+}
+// Four chunks of a pair as bf16, and their store: rows i = 4 half ..+3 of pairs 0-2, all of
+// pair 3's codes.  Lanes 4-7 of eight store their two 16-byte pieces in the other order, so
+// that eight lanes hit 128 distinct bytes.
+__device__ __forceinline__ void convert_fp8(const uint4 (&st)[kStage], const uint2& sc, bool slow, int mb,
+                                            int half, uint4 (&cv)[8], int lane) {
+  const uint32_t word = mb < 2 ? sc.x : sc.y;      // groups 4 (mb / 2) ..+3
+  const int shift = mb < 3 ? 16 * (mb & 1) + 8 * ((lane >> 2) & 1) : 16;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const int i = 4 * half + x;
+    const uint4 v = st[mb < 3 ? 8 * mb + i : x];
+    const uint32_t sb = (__shfl_sync(0xffffffffu, word, mb < 3 ? 4 * i + (lane >> 3) : 8 * x + (lane >> 2)) >> shift) & 0xffu;
+    uint2 a, b, c, d;
+    if (!slow) {                                   // uniform over the warp
+      const uint32_t s = (sb - 112u) * 0x04000400u;
+      a = codes_fast(v.x, s); b = codes_fast(v.y, s); c = codes_fast(v.z, s); d = codes_fast(v.w, s);
+    } else {
+      a = codes_slow(v.x, sb); b = codes_slow(v.y, sb); c = codes_slow(v.z, sb); d = codes_slow(v.w, sb);
+    }
+    cv[2 * x] = make_uint4(a.x, a.y, b.x, b.y);
+    cv[2 * x + 1] = make_uint4(c.x, c.y, d.x, d.y);
   }
 }
-__device__ __forceinline__ void sts16(uint8_t* d, const uint4& v) { sts16(d, v.x, v.y, v.z, v.w); }
 __device__ __forceinline__ void store_fp8(const uint4 (&cv)[8], int mb, int half, uint8_t* sKV, int row0,
                                           int lane) {
+  const int sw = mb < 3 ? (lane >> 2) & 1 : 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int x = 4 * half + i;
-    const int r = row0 + (mb < 3 ? fp8_row(x, lane) : 8 * x + (lane >> 2));
-    const int ch = mb < 3 ? fp8_chunk(lane) : lane & 3;
-    sts16(tile_at(sKV, r, 2 * mb + (ch >> 2), 2 * (ch & 3)), cv[2 * i]);
-    sts16(tile_at(sKV, r, 2 * mb + (ch >> 2), 2 * (ch & 3) + 1), cv[2 * i + 1]);
+  for (int x = 0; x < 4; ++x) {
+    const int r = row0 + (mb < 3 ? 4 * (4 * half + x) + (lane >> 3) : 8 * x + (lane >> 2));
+    const int cb = 2 * mb + sw, cc = 2 * (lane & 3);
+    const uint4 u = cv[2 * x], v = cv[2 * x + 1];
+    sts16(tile_at(sKV, r, cb, cc + sw), sw ? v : u);
+    sts16(tile_at(sKV, r, cb, cc + (sw ^ 1)), sw ? u : v);
   }
 }
 __device__ __forceinline__ void store_hi(const uint4 (&st)[kStage], uint8_t* sKV, int row0, int lane) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sts16(tile_at(sKV, row0 + 4 * i + (lane >> 3), 7, lane & 7), st[4 + i]);
+  for (int i = 0; i < 8; ++i) sts16(tile_at(sKV, row0 + 4 * i + (lane >> 3), 7, lane & 7), st[8 + i]);
 }
 
 // This thread's part of a pair is in shared memory: publish it to the tensor core and arrive
@@ -432,8 +475,9 @@ __global__ void __launch_bounds__(kLaunch, 1)
     const int row0 = qd * 32;
     bool ok = true;
     uint4 st[kStage];
-    uint2 sc = make_uint2(0u, 0u);
-    uint64_t src = 0;
+    uint2 sc = make_uint2(0u, 0u);                 // FP8: the scales of this lane's row, and the
+    int c8[8];                                     // numbers of the eight rows it loads
+    RowPtrs rp;
     Stream S;
     S.item = blockIdx.x;
     S.live = S.item < p.items;
@@ -463,10 +507,11 @@ __global__ void __launch_bounds__(kLaunch, 1)
       // 128 consecutive rows of one page that all exist come by TMA, straight into the tile
       whole = !FP8 && !window && !p.idx && (S.tile + 1) * kRows <= S.it.nsel && have == 0xffffffffu;
       if (FP8 && !window) {
-        load_fp8(st, sc, p, code, lane);
+        load_fp8(st, sc, c8, p, code, lane);
       } else if (!whole) {
-        src = row_addr(p, window, code);
-        load_bf16(st, 0, 2, src, lane);
+        row_ptrs(rp, row_addr(p, window, code), lane);
+        load_bf16(st, 0, rp);
+        load_bf16(st, 1, rp);
       }
       if (!new_q) {
         ++S.tile;
@@ -509,11 +554,12 @@ __global__ void __launch_bounds__(kLaunch, 1)
         }
         ++n_tma;
       } else {
+        const bool slow = FP8 && !window && !__all_sync(0xffffffffu, scales_fast(sc));
 #pragma unroll
         for (int mb = 0; mb < 4; ++mb) {
           const bool fp8 = FP8 && !window;
           uint4 cv[8];
-          if (fp8) convert_fp8(st, sc, mb, 0, cv, lane);
+          if (fp8) convert_fp8(st, sc, slow, mb, 0, cv, lane);
           if (n > 0) {
             ok = ok && tc::mbar_wait_hint(bar_pv + mb, (n - 1) & 1, p.err, kHintNs);
             tc::tc_fence_after();
@@ -521,7 +567,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
           if (fp8) {
             store_fp8(cv, mb, 0, sKV, row0, lane);
             if (mb < 3) {
-              convert_fp8(st, sc, mb, 1, cv, lane);
+              convert_fp8(st, sc, slow, mb, 1, cv, lane);
               store_fp8(cv, mb, 1, sKV, row0, lane);
             } else {
               store_hi(st, sKV, row0, lane);
@@ -534,8 +580,8 @@ __global__ void __launch_bounds__(kLaunch, 1)
             if (wait_q) tc::cp_async_wait_all();
           }
           pair_landed(mb);
-          if (!fp8 && mb < 2) load_bf16(st, mb + 2, 1, src, lane);
-          if (fp8 && mb == 1) load_fp8_last(st, p, code, lane);
+          if (!fp8 && mb < 2) load_bf16(st, mb + 2, rp);
+          if (fp8 && mb == 1) load_fp8_last(st, c8, p, lane);
           if (mb == 2) row_page(nx, S.it.seq, p);
         }
       }
@@ -582,6 +628,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
             lg[h + 1] = __float_as_uint(fmaf(__uint_as_float(lg[h + 1]), p.scale_log2, -M4.y));
             lg[h + 2] = __float_as_uint(fmaf(__uint_as_float(lg[h + 2]), p.scale_log2, -M4.z));
             lg[h + 3] = __float_as_uint(fmaf(__uint_as_float(lg[h + 3]), p.scale_log2, -M4.w));
+            if (h % 8 == 4) asm volatile("" ::: "memory");   // not all references in registers at once
           }
           if (!full) {
 #pragma unroll
@@ -629,18 +676,19 @@ __global__ void __launch_bounds__(kLaunch, 1)
           }
           tc::named_bar(3, kST);
           if (started && s_flag[0]) {
-            for (int mb = 2 * hf; mb < 2 * hf + 2; ++mb) {
+#pragma unroll 1
+            for (int x = 0; x < 4; ++x) {          // this half's two dim blocks, 32 heads each time
+              uint32_t o[32];
+              const uint32_t ta = tO + 2 * hf * kH + x * 32 + lane_addr;
+              const float* al = s_alpha + 32 * (x & 1);
+              tc::tmem_ld32(ta, o);
+              tc::tmem_ld_wait(o);
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                uint32_t o[32];
-                const uint32_t ta = tO + mb * kH + half * 32 + lane_addr;
-                tc::tmem_ld32(ta, o);
-                tc::tmem_ld_wait(o);
-#pragma unroll
-                for (int h = 0; h < 32; ++h)
-                  o[h] = __float_as_uint(__uint_as_float(o[h]) * s_alpha[half * 32 + h]);
-                tc::tmem_st32(ta, o);
+              for (int h = 0; h < 32; ++h) {
+                o[h] = __float_as_uint(__uint_as_float(o[h]) * al[h]);
+                if (h % 8 == 7) asm volatile("" ::: "memory");
               }
+              tc::tmem_st32(ta, o);
             }
             tc::tmem_st_wait();
 #pragma unroll
