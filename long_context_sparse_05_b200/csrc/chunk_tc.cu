@@ -258,7 +258,8 @@ __device__ __forceinline__ void load_fp8(uint4 (&st)[kStage], uint2& sc, int (&c
     for (int mb = 0; mb < 3; ++mb) st[8 * mb + i] = ldg_stream(a + 128 * mb);
   }
 }
-// Pair 3: lanes 0-3 of eight take the row's codes, and all eight its bf16 dims.
+// Pair 3 into st[8..19]: four chunks of codes, lane = (row of eight, chunk of four), then the
+// eight rows' bf16 dims.
 __device__ __forceinline__ void load_fp8_last(uint4 (&st)[kStage], const int (&c)[8], const ChunkTc& p,
                                               int lane) {
 #pragma unroll
@@ -266,16 +267,15 @@ __device__ __forceinline__ void load_fp8_last(uint4 (&st)[kStage], const int (&c
     const uint8_t* h = c[i] >= 0 ? reinterpret_cast<const uint8_t*>(static_cast<const __nv_bfloat16*>(p.kv.hi) +
                                                                     (long long)c[i] * kHi)
                                  : g_zero_row;
-    st[8 + i] = ldg_stream(h + 16 * (lane & 7));
+    st[12 + i] = ldg_stream(h + 16 * (lane & 7));
   }
-  // codes: lane = (row of eight, chunk of four), so rows 8 i + lane / 4
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int x = __shfl_sync(0xffffffffu, c[2 * i], ((lane >> 2) & 3) * 8);
     const int y = __shfl_sync(0xffffffffu, c[2 * i + 1], ((lane >> 2) & 3) * 8);
     const int r = lane & 16 ? y : x;
-    st[i] = ldg_stream((r >= 0 ? static_cast<const uint8_t*>(p.kv.rows) + (long long)r * kNc + 384 : g_zero_row) +
-                       16 * (lane & 3));
+    st[8 + i] = ldg_stream((r >= 0 ? static_cast<const uint8_t*>(p.kv.rows) + (long long)r * kNc + 384 : g_zero_row) +
+                           16 * (lane & 3));
   }
 }
 // Four codes times 2^k as four bf16 values, exactly.  Fast: two codes to f16 in one conversion,
@@ -311,35 +311,31 @@ __device__ __forceinline__ bool scales_fast(const uint2& sc) {
   for (int g = 0; g < 7; ++g) ok &= (((g < 4 ? sc.x : sc.y) >> (8 * (g & 3))) & 0xffu) - 113u <= 142u - 113u;
   return ok;
 }
-// Four chunks of a pair as bf16, and their store: rows i = 4 half ..+3 of pairs 0-2, all of
-// pair 3's codes.  Lanes 4-7 of eight store their two 16-byte pieces in the other order, so
-// that eight lanes hit 128 distinct bytes.
-__device__ __forceinline__ void convert_fp8(const uint4 (&st)[kStage], const uint2& sc, bool slow, int mb,
-                                            int half, uint4 (&cv)[8], int lane) {
+// Four of the lane's chunks, st[4 half ..+3], as bf16, and their store: rows i = 4 half ..+3
+// of pair mb (kLast: pair 3's codes).  Lanes 4-7 of eight store their two 16-byte pieces in the
+// other order, so that eight lanes hit 128 distinct bytes.
+template <bool kLast>
+__device__ __forceinline__ void convert_fp8(const uint4 (&st)[kStage], const uint2& sc, int mb, int half,
+                                            uint4 (&cv)[8], int lane) {
   const uint32_t word = mb < 2 ? sc.x : sc.y;      // groups 4 (mb / 2) ..+3
-  const int shift = mb < 3 ? 16 * (mb & 1) + 8 * ((lane >> 2) & 1) : 16;
+  const int shift = kLast ? 16 : 16 * (mb & 1) + 8 * ((lane >> 2) & 1);
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
-    const int i = 4 * half + x;
-    const uint4 v = st[mb < 3 ? 8 * mb + i : x];
-    const uint32_t sb = (__shfl_sync(0xffffffffu, word, mb < 3 ? 4 * i + (lane >> 3) : 8 * x + (lane >> 2)) >> shift) & 0xffu;
-    uint2 a, b, c, d;
-    if (!slow) {                                   // uniform over the warp
-      const uint32_t s = (sb - 112u) * 0x04000400u;
-      a = codes_fast(v.x, s); b = codes_fast(v.y, s); c = codes_fast(v.z, s); d = codes_fast(v.w, s);
-    } else {
-      a = codes_slow(v.x, sb); b = codes_slow(v.y, sb); c = codes_slow(v.z, sb); d = codes_slow(v.w, sb);
-    }
+    const uint4 v = st[4 * half + x];
+    const int row = kLast ? 8 * x + (lane >> 2) : 4 * (4 * half + x) + (lane >> 3);
+    const uint32_t s = (((__shfl_sync(0xffffffffu, word, row) >> shift) & 0xffu) - 112u) * 0x04000400u;
+    const uint2 a = codes_fast(v.x, s), b = codes_fast(v.y, s), c = codes_fast(v.z, s), d = codes_fast(v.w, s);
     cv[2 * x] = make_uint4(a.x, a.y, b.x, b.y);
     cv[2 * x + 1] = make_uint4(c.x, c.y, d.x, d.y);
   }
 }
+template <bool kLast>
 __device__ __forceinline__ void store_fp8(const uint4 (&cv)[8], int mb, int half, uint8_t* sKV, int row0,
                                           int lane) {
-  const int sw = mb < 3 ? (lane >> 2) & 1 : 0;
+  const int sw = kLast ? 0 : (lane >> 2) & 1;
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
-    const int r = row0 + (mb < 3 ? 4 * (4 * half + x) + (lane >> 3) : 8 * x + (lane >> 2));
+    const int r = row0 + (kLast ? 8 * x + (lane >> 2) : 4 * (4 * half + x) + (lane >> 3));
     const int cb = 2 * mb + sw, cc = 2 * (lane & 3);
     const uint4 u = cv[2 * x], v = cv[2 * x + 1];
     sts16(tile_at(sKV, r, cb, cc + sw), sw ? v : u);
@@ -348,7 +344,26 @@ __device__ __forceinline__ void store_fp8(const uint4 (&cv)[8], int mb, int half
 }
 __device__ __forceinline__ void store_hi(const uint4 (&st)[kStage], uint8_t* sKV, int row0, int lane) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sts16(tile_at(sKV, row0 + 4 * i + (lane >> 3), 7, lane & 7), st[8 + i]);
+  for (int i = 0; i < 8; ++i) sts16(tile_at(sKV, row0 + 4 * i + (lane >> 3), 7, lane & 7), st[4 + i]);
+}
+// A quarter's part of a pair straight from memory, for a tile with a scale that codes_fast does
+// not take: lane's row, one chunk after another.
+__device__ __noinline__ void move_fp8_slow(const ChunkTc& p, int code, int mb, uint8_t* sKV, int row) {
+  const long long c = code;
+#pragma unroll 1
+  for (int x = 0; x < 16; ++x) {                   // 16-byte pieces of the row's 128 dims
+    const int d = 128 * mb + 8 * x;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (code >= 0 && d >= kNc) {
+      v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.kv.hi) + c * kHi + (d - kNc));
+    } else if (code >= 0) {
+      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.kv.rows) + c * kNc + d);
+      const uint32_t sb = static_cast<const uint8_t*>(p.kv.scales)[c * 8 + d / kScaleGroup];
+      const uint2 a = codes_slow(w.x, sb), b = codes_slow(w.y, sb);
+      v = make_uint4(a.x, a.y, b.x, b.y);
+    }
+    sts16(tile_at(sKV, row, 2 * mb + (x >> 3), x & 7), v);
+  }
 }
 
 // This thread's part of a pair is in shared memory: publish it to the tensor core and arrive
@@ -440,23 +455,24 @@ __global__ void __launch_bounds__(kLaunch, 1)
       const Item I = get_item(p, cu, pos0, item, lane);
       if (!I.live) break;
       for (int j = I.tb; j < I.te; ++j) {
-#pragma unroll
+#pragma unroll 1
         for (int mb = 0; mb < 4; ++mb) {
           tc::named_bar(4 + mb, kBarP);             // the pair (and, with the first, q) is in place
           tc::tc_fence_after();
 #pragma unroll
-          for (int kb = 2 * mb; kb < 2 * mb + 2; ++kb) {
+          for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              tc::mma_f16_el(uS, tc::desc_advance(dS_a, kb * kKVBlk + kk * 32),
-                             tc::desc_advance(dS_b, kb * kQBlk + kk * 32), idS, (kb | kk) != 0, el);
+              tc::mma_f16_el(uS, tc::desc_advance(dS_a, (2 * mb + kb) * kKVBlk + kk * 32),
+                             tc::desc_advance(dS_b, (2 * mb + kb) * kQBlk + kk * 32), idS, (mb | kb | kk) != 0,
+                             el);
           }
         }
         if (el) tc::mma_commit(bar_s);
         __syncwarp();
         tc::named_bar(2, kBarS);                    // P^T in place, O^T rescaled
         tc::tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int mb = 0; mb < 4; ++mb) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
@@ -553,35 +569,55 @@ __global__ void __launch_bounds__(kLaunch, 1)
           pair_landed(mb);
         }
         ++n_tma;
-      } else {
-        const bool slow = FP8 && !window && !__all_sync(0xffffffffu, scales_fast(sc));
-#pragma unroll
+      } else if (FP8 && !window) {
+        // one copy of the code for pairs 0-2 (the staged registers move up a pair each time):
+        // unrolled, the producers' instructions did not stay in the instruction cache
+        const bool fast = __all_sync(0xffffffffu, scales_fast(sc));
+#pragma unroll 1
         for (int mb = 0; mb < 4; ++mb) {
-          const bool fp8 = FP8 && !window;
           uint4 cv[8];
-          if (fp8) convert_fp8(st, sc, slow, mb, 0, cv, lane);
+          if (fast) {
+            if (mb < 3) convert_fp8<false>(st, sc, mb, 0, cv, lane);
+            else convert_fp8<true>(st, sc, mb, 0, cv, lane);
+          }
           if (n > 0) {
             ok = ok && tc::mbar_wait_hint(bar_pv + mb, (n - 1) & 1, p.err, kHintNs);
             tc::tc_fence_after();
           }
-          if (fp8) {
-            store_fp8(cv, mb, 0, sKV, row0, lane);
-            if (mb < 3) {
-              convert_fp8(st, sc, slow, mb, 1, cv, lane);
-              store_fp8(cv, mb, 1, sKV, row0, lane);
-            } else {
-              store_hi(st, sKV, row0, lane);
-            }
+          if (!fast) {
+            move_fp8_slow(p, code, mb, sKV, row0 + lane);
+          } else if (mb < 3) {
+            store_fp8<false>(cv, mb, 0, sKV, row0, lane);
+            convert_fp8<false>(st, sc, mb, 1, cv, lane);
+            store_fp8<false>(cv, mb, 1, sKV, row0, lane);
           } else {
-            store_bf16(st, mb, sKV, row0, lane);
+            store_fp8<true>(cv, mb, 0, sKV, row0, lane);
+            store_hi(st, sKV, row0, lane);
           }
           if (mb == 0) {
             if (lane == 0) s_valid[qd] = have;
             if (wait_q) tc::cp_async_wait_all();
           }
           pair_landed(mb);
-          if (!fp8 && mb < 2) load_bf16(st, mb + 2, rp);
-          if (fp8 && mb == 1) load_fp8_last(st, c8, p, lane);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) st[i] = st[i + 8];
+          if (mb == 1) load_fp8_last(st, c8, p, lane);
+          if (mb == 2) row_page(nx, S.it.seq, p);
+        }
+      } else {
+#pragma unroll
+        for (int mb = 0; mb < 4; ++mb) {
+          if (n > 0) {
+            ok = ok && tc::mbar_wait_hint(bar_pv + mb, (n - 1) & 1, p.err, kHintNs);
+            tc::tc_fence_after();
+          }
+          store_bf16(st, mb, sKV, row0, lane);
+          if (mb == 0) {
+            if (lane == 0) s_valid[qd] = have;
+            if (wait_q) tc::cp_async_wait_all();
+          }
+          pair_landed(mb);
+          if (mb < 2) load_bf16(st, mb + 2, rp);
           if (mb == 2) row_page(nx, S.it.seq, p);
         }
       }
@@ -752,6 +788,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
       }
       tc::named_bar(3, kST);
       if (p.nsplit > 1) {
+#pragma unroll 1
         for (int mb = 2 * hf; mb < 2 * hf + 2; ++mb) {
           ok = ok && tc::mbar_wait_hint(bar_pv + mb, (ns - 1) & 1, p.err, kHintNs);
           tc::tc_fence_after();
@@ -769,6 +806,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
           }
         }
       } else {
+#pragma unroll 1
         for (int mb = 0; mb < 4; ++mb) {
           ok = ok && tc::mbar_wait_hint(bar_pv + mb, (ns - 1) & 1, p.err, kHintNs);
           tc::tc_fence_after();
