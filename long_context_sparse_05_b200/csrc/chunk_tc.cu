@@ -27,8 +27,8 @@
 // an item: the reduction over the rows runs once per item, so an ordinary tile needs one
 // barrier (the OR of "some logit exceeds the maximum") before its probabilities.
 //
-// CTA: warps 0-7 softmax and output (two per TMEM lane quarter, 32 heads each), warps 8-11
-// producers, warp 12 issues every MMA (13-15 idle: register shares go by warpgroup).
+// CTA: warps 0-7 softmax and output (two per TMEM lane quarter, 32 heads each), warps 8-15
+// producers, warp 16 issues every MMA (17-19 idle: register shares go by warpgroup).
 // Producers walk the CTA's tiles as one stream across its items.
 //
 // Work item = (token, split of its tiles); CTAs walk the items with stride gridDim.x.  Few
@@ -58,18 +58,18 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;      // log2 units
 constexpr int kSW = 8;                // softmax warps
-constexpr int kPW = 4;                // producer warps, one per quarter of a tile's rows
+constexpr int kPW = 8;                // producer warps, each 16 of a tile's rows
 constexpr int kST = 32 * kSW;
 constexpr int kBarS = kST + 32;       // threads of a barrier of the softmax and the MMA warp
 constexpr int kBarP = 32 * kPW + 32;  // ... of the producers and the MMA warp
-constexpr int kLaunch = 512;
-// Registers a thread by warpgroup (2 x softmax, producers, MMA), out of 4 x 128 at launch.
-constexpr int kRegsSoftmax = 120, kRegsProd = 232, kRegsMma = 40;
-constexpr int kRegsLaunch = 128;      // 65,536 / 512
+constexpr int kLaunch = 640;
+// Registers a thread by warpgroup (2 x softmax, 2 x producers, MMA), out of 5 x 96 at launch.
+constexpr int kRegsSoftmax = 96, kRegsProd = 128, kRegsMma = 32;
+constexpr int kRegsLaunch = 96;       // 65,536 / 640, whole multiples of 8
 // .dec must not raise a warpgroup's count and .inc must not lower it (either faults), and the
 // shares must fit what the block was launched with (or .inc waits for good).
-static_assert(kRegsSoftmax <= kRegsLaunch && kRegsMma <= kRegsLaunch && kRegsProd >= kRegsLaunch &&
-                  2 * kRegsSoftmax + kRegsProd + kRegsMma <= 4 * kRegsLaunch, "setmaxnreg shares");
+static_assert(kRegsSoftmax >= kRegsLaunch && kRegsProd >= kRegsLaunch && kRegsMma <= kRegsLaunch &&
+                  2 * kRegsSoftmax + 2 * kRegsProd + kRegsMma <= 5 * kRegsLaunch, "setmaxnreg shares");
 constexpr uint32_t kHintNs = 64;
 constexpr int kSeqCache = 1024;       // sequences whose boundaries are kept in shared memory
 constexpr int kMaxSplit = 32;
@@ -194,87 +194,80 @@ __device__ __forceinline__ uint8_t* tile_at(uint8_t* sKV, int row, int cb, int c
   return sKV + cb * kKVBlk + row * 128 + ((cc ^ (row & 7)) << 4);
 }
 
-constexpr int kStage = 32;   // 16-byte registers a producer thread stages of the next tile
+constexpr int kStage = 16;   // 16-byte registers a producer thread stages of the next tile
 
-// Producer warp qd moves rows 32 qd ..+31 of the tile; lane = (row of four, 16-byte chunk of
-// eight): rows 4 i + lane / 8, i < 8, 128 contiguous bytes of a row at a time (64-byte pieces
+// A producer warp moves 16 rows of the tile; lane = (row of four, 16-byte chunk of eight): rows
+// 4 i + lane / 8, i < 4, 128 contiguous bytes of a row at a time (64-byte pieces
 // take twice the tag lookups: 1,200 instead of 600 cycles for a tile's 128 loads).  The rows'
 // places are shuffled to their lanes ahead of all loads: a shuffle between loads waits behind
 // them in the same queue.
 //
 // bf16 rows: two of a tile's four 128-dim pairs are staged; the other two are loaded into
 // their registers as those are stored.
-struct RowPtrs { const char* a[8]; };
-__device__ __forceinline__ void row_ptrs(RowPtrs& r, uint64_t src, int lane) {
+// Numbers of the four rows this lane loads.
+__device__ __forceinline__ void row_numbers(int (&c)[4], int code, int lane) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint64_t x = __shfl_sync(0xffffffffu, src, 4 * i + (lane >> 3));
-    r.a[i] = reinterpret_cast<const char*>(x) + 16 * (lane & 7);
-  }
+  for (int i = 0; i < 4; ++i) c[i] = __shfl_sync(0xffffffffu, code, 4 * i + (lane >> 3));
 }
-__device__ __forceinline__ void load_bf16(uint4 (&st)[kStage], int mb, const RowPtrs& r) {
+// Address of a plain row: in the pool, in new_win or in the rings.
+__device__ __forceinline__ const char* row_addr(const ChunkTc& p, bool window, int code) {
+  const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(p.kv.rows);
+  if (window) base = code >= kNewTag ? p.new_win : p.win;
+  const char* a = reinterpret_cast<const char*>(base + (long long)(window ? code & (kNewTag - 1) : code) * kD);
+  return code < 0 ? reinterpret_cast<const char*>(g_zero_row) : a;
+}
+__device__ __forceinline__ void load_bf16(uint4 (&st)[kStage], int mb, const ChunkTc& p, bool window,
+                                          const int (&c)[4], int lane) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
+    const char* a = row_addr(p, window, c[i]) + 16 * (lane & 7) + 256 * mb;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) st[16 * (mb & 1) + 2 * i + j] = ldg_stream(r.a[i] + 256 * mb + 128 * j);
+    for (int j = 0; j < 2; ++j) st[8 * (mb & 1) + 2 * i + j] = ldg_stream(a + 128 * j);
   }
 }
 __device__ __forceinline__ void sts16(uint8_t* d, const uint4& v) { sts16(d, v.x, v.y, v.z, v.w); }
 __device__ __forceinline__ void store_bf16(const uint4 (&st)[kStage], int mb, uint8_t* sKV, int row0,
                                            int lane) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      sts16(tile_at(sKV, row0 + 4 * i + (lane >> 3), 2 * mb + j, lane & 7), st[16 * (mb & 1) + 2 * i + j]);
+      sts16(tile_at(sKV, row0 + 4 * i + (lane >> 3), 2 * mb + j, lane & 7), st[8 * (mb & 1) + 2 * i + j]);
   }
 }
-// Address of a plain row: in the pool, in new_win or in the rings.
-__device__ __forceinline__ uint64_t row_addr(const ChunkTc& p, bool window, int code) {
-  if (code < 0) return reinterpret_cast<uint64_t>(g_zero_row);
-  const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(p.kv.rows);
-  if (window) {
-    base = code >= kNewTag ? p.new_win : p.win;
-    code &= kNewTag - 1;
-  }
-  return reinterpret_cast<uint64_t>(base + (long long)code * kD);
-}
-
 // FP8 rows: pairs 0-2 are staged (a row's 128 codes of a pair are eight lanes' chunks); pair 3
 // (the last 64 codes and the 64 bf16 dims) is loaded into the registers of pairs 0 and 1 as
 // those are stored.  The scale words of the quarter's rows stay with their rows' lanes.
-__device__ __forceinline__ void load_fp8(uint4 (&st)[kStage], uint2& sc, int (&c)[8], const ChunkTc& p,
+__device__ __forceinline__ void load_fp8(uint4 (&st)[kStage], uint2& sc, const int (&c)[4], const ChunkTc& p,
                                          int code, int lane) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] = __shfl_sync(0xffffffffu, code, 4 * i + (lane >> 3));
   sc = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);       // a row that does not exist: zeros times 1
   if (code >= 0)
     sc = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.kv.scales) + (long long)code * 8));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const uint8_t* a = (c[i] >= 0 ? static_cast<const uint8_t*>(p.kv.rows) + (long long)c[i] * kNc : g_zero_row) +
                        16 * (lane & 7);
 #pragma unroll
-    for (int mb = 0; mb < 3; ++mb) st[8 * mb + i] = ldg_stream(a + 128 * mb);
+    for (int mb = 0; mb < 3; ++mb) st[4 * mb + i] = ldg_stream(a + 128 * mb);
   }
 }
-// Pair 3 into st[8..19]: four chunks of codes, lane = (row of eight, chunk of four), then the
-// eight rows' bf16 dims.
-__device__ __forceinline__ void load_fp8_last(uint4 (&st)[kStage], const int (&c)[8], const ChunkTc& p,
+// Pair 3 into st[4..9]: two chunks of codes, lane = (row of eight, chunk of four), then the four
+// rows' bf16 dims.
+__device__ __forceinline__ void load_fp8_last(uint4 (&st)[kStage], const int (&c)[4], const ChunkTc& p,
                                               int lane) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const uint8_t* h = c[i] >= 0 ? reinterpret_cast<const uint8_t*>(static_cast<const __nv_bfloat16*>(p.kv.hi) +
                                                                     (long long)c[i] * kHi)
                                  : g_zero_row;
-    st[12 + i] = ldg_stream(h + 16 * (lane & 7));
+    st[6 + i] = ldg_stream(h + 16 * (lane & 7));
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const int x = __shfl_sync(0xffffffffu, c[2 * i], ((lane >> 2) & 3) * 8);
     const int y = __shfl_sync(0xffffffffu, c[2 * i + 1], ((lane >> 2) & 3) * 8);
     const int r = lane & 16 ? y : x;
-    st[8 + i] = ldg_stream((r >= 0 ? static_cast<const uint8_t*>(p.kv.rows) + (long long)r * kNc + 384 : g_zero_row) +
+    st[4 + i] = ldg_stream((r >= 0 ? static_cast<const uint8_t*>(p.kv.rows) + (long long)r * kNc + 384 : g_zero_row) +
                            16 * (lane & 3));
   }
 }
@@ -311,18 +304,18 @@ __device__ __forceinline__ bool scales_fast(const uint2& sc) {
   for (int g = 0; g < 7; ++g) ok &= (((g < 4 ? sc.x : sc.y) >> (8 * (g & 3))) & 0xffu) - 113u <= 142u - 113u;
   return ok;
 }
-// Four of the lane's chunks, st[4 half ..+3], as bf16, and their store: rows i = 4 half ..+3
-// of pair mb (kLast: pair 3's codes).  Lanes 4-7 of eight store their two 16-byte pieces in the
-// other order, so that eight lanes hit 128 distinct bytes.
+// Two of the lane's chunks of a pair, st[2 half ..+1] (kLast: pair 3's codes, half 0 alone), as
+// bf16, and their store.  Lanes 4-7 of eight store their two 16-byte pieces in the other order,
+// so that eight lanes hit 128 distinct bytes.
 template <bool kLast>
 __device__ __forceinline__ void convert_fp8(const uint4 (&st)[kStage], const uint2& sc, int mb, int half,
-                                            uint4 (&cv)[8], int lane) {
+                                            uint4 (&cv)[4], int lane) {
   const uint32_t word = mb < 2 ? sc.x : sc.y;      // groups 4 (mb / 2) ..+3
   const int shift = kLast ? 16 : 16 * (mb & 1) + 8 * ((lane >> 2) & 1);
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    const uint4 v = st[4 * half + x];
-    const int row = kLast ? 8 * x + (lane >> 2) : 4 * (4 * half + x) + (lane >> 3);
+  for (int x = 0; x < 2; ++x) {
+    const uint4 v = st[2 * half + x];
+    const int row = kLast ? 8 * x + (lane >> 2) : 4 * (2 * half + x) + (lane >> 3);
     const uint32_t s = (((__shfl_sync(0xffffffffu, word, row) >> shift) & 0xffu) - 112u) * 0x04000400u;
     const uint2 a = codes_fast(v.x, s), b = codes_fast(v.y, s), c = codes_fast(v.z, s), d = codes_fast(v.w, s);
     cv[2 * x] = make_uint4(a.x, a.y, b.x, b.y);
@@ -330,12 +323,12 @@ __device__ __forceinline__ void convert_fp8(const uint4 (&st)[kStage], const uin
   }
 }
 template <bool kLast>
-__device__ __forceinline__ void store_fp8(const uint4 (&cv)[8], int mb, int half, uint8_t* sKV, int row0,
+__device__ __forceinline__ void store_fp8(const uint4 (&cv)[4], int mb, int half, uint8_t* sKV, int row0,
                                           int lane) {
   const int sw = kLast ? 0 : (lane >> 2) & 1;
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    const int r = row0 + (kLast ? 8 * x + (lane >> 2) : 4 * (4 * half + x) + (lane >> 3));
+  for (int x = 0; x < 2; ++x) {
+    const int r = row0 + (kLast ? 8 * x + (lane >> 2) : 4 * (2 * half + x) + (lane >> 3));
     const int cb = 2 * mb + sw, cc = 2 * (lane & 3);
     const uint4 u = cv[2 * x], v = cv[2 * x + 1];
     sts16(tile_at(sKV, r, cb, cc + sw), sw ? v : u);
@@ -344,14 +337,14 @@ __device__ __forceinline__ void store_fp8(const uint4 (&cv)[8], int mb, int half
 }
 __device__ __forceinline__ void store_hi(const uint4 (&st)[kStage], uint8_t* sKV, int row0, int lane) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sts16(tile_at(sKV, row0 + 4 * i + (lane >> 3), 7, lane & 7), st[4 + i]);
+  for (int i = 0; i < 4; ++i) sts16(tile_at(sKV, row0 + 4 * i + (lane >> 3), 7, lane & 7), st[2 + i]);
 }
-// A quarter's part of a pair straight from memory, for a tile with a scale that codes_fast does
-// not take: lane's row, one chunk after another.
-__device__ __noinline__ void move_fp8_slow(const ChunkTc& p, int code, int mb, uint8_t* sKV, int row) {
+// A warp's part of a pair straight from memory, for a tile with a scale that codes_fast does
+// not take: lane = (row of 16, half of the pair's dims), one 16-byte piece after another.
+__device__ __forceinline__ void move_fp8_slow(const ChunkTc& p, int code, int mb, uint8_t* sKV, int row, int half) {
   const long long c = code;
 #pragma unroll 1
-  for (int x = 0; x < 16; ++x) {                   // 16-byte pieces of the row's 128 dims
+  for (int x = 8 * half; x < 8 * half + 8; ++x) {
     const int d = 128 * mb + 8 * x;
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
     if (code >= 0 && d >= kNc) {
@@ -362,7 +355,7 @@ __device__ __noinline__ void move_fp8_slow(const ChunkTc& p, int code, int mb, u
       const uint2 a = codes_slow(w.x, sb), b = codes_slow(w.y, sb);
       v = make_uint4(a.x, a.y, b.x, b.y);
     }
-    sts16(tile_at(sKV, row, 2 * mb + (x >> 3), x & 7), v);
+    sts16(tile_at(sKV, row, 2 * mb + half, x & 7), v);
   }
 }
 
@@ -414,6 +407,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
   uint64_t* bar_full = bar_pv + 4;                // [4]: a pair's TMA copies have landed
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bar_full + 4);
   uint32_t* s_valid = tmem_holder + 2;            // [4] the tile's rows that exist, a bit each
+  uint16_t* s_valid16 = reinterpret_cast<uint16_t*>(s_valid);   // ... as the producers write them
   int32_t* s_cu = reinterpret_cast<int32_t*>(s_valid + 4);   // [kSeqCache + 1]
   int32_t* s_pos0 = s_cu + kSeqCache + 1;         // [kSeqCache]
 
@@ -487,13 +481,13 @@ __global__ void __launch_bounds__(kLaunch, 1)
   } else if (warp >= kSW) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsProd));
     // ------------------------------------------------------------------ producers
-    const int qd = warp - kSW;                     // this warp's quarter of a tile's rows
-    const int row0 = qd * 32;
+    const int w = warp - kSW;
+    const int row0 = 16 * w;                       // this warp's rows of a tile
+    const int myrow = row0 + (lane & 15);          // the one whose place this lane finds out
     bool ok = true;
     uint4 st[kStage];
     uint2 sc = make_uint2(0u, 0u);                 // FP8: the scales of this lane's row, and the
-    int c8[8];                                     // numbers of the eight rows it loads
-    RowPtrs rp;
+    int c4[4];                                     // numbers of the four rows it loads
     Stream S;
     S.item = blockIdx.x;
     S.live = S.item < p.items;
@@ -506,11 +500,11 @@ __global__ void __launch_bounds__(kLaunch, 1)
     }
     // the first tile's row numbers, loads and queries, then the second tile's rows
     RowRef nx;
-    row_entry(nx, S, p, qd * 32 + lane);
+    row_entry(nx, S, p, myrow);
     row_page(nx, S.it.seq, p);
     int code = -1;
     bool window = false, whole = false, live = false, new_q = false;
-    uint32_t have = 0;                             // rows of the quarter that exist
+    uint32_t have = 0;                             // rows that exist (twice 16 bits)
     int item = -1;
     auto take = [&]() {   // nx becomes the staged tile; its loads go out; nx is the next one's entries
       live = S.live;
@@ -522,25 +516,25 @@ __global__ void __launch_bounds__(kLaunch, 1)
       have = __ballot_sync(0xffffffffu, code >= 0);
       // 128 consecutive rows of one page that all exist come by TMA, straight into the tile
       whole = !FP8 && !window && !p.idx && (S.tile + 1) * kRows <= S.it.nsel && have == 0xffffffffu;
+      row_numbers(c4, code, lane);
       if (FP8 && !window) {
-        load_fp8(st, sc, c8, p, code, lane);
+        load_fp8(st, sc, c4, p, code, lane);
       } else if (!whole) {
-        row_ptrs(rp, row_addr(p, window, code), lane);
-        load_bf16(st, 0, rp);
-        load_bf16(st, 1, rp);
+        load_bf16(st, 0, p, window, c4, lane);
+        load_bf16(st, 1, p, window, c4, lane);
       }
       if (!new_q) {
         ++S.tile;
         stream_settle(S, p, cu, pos0, lane);
-        row_entry(nx, S, p, qd * 32 + lane);
+        row_entry(nx, S, p, myrow);
       }
     };
     auto queries = [&]() {   // the item's first tile: its queries too
       if (!live || !new_q) return;
-      load_q(p, S.it.tok, sQ, qd, lane);
+      load_q(p, S.it.tok, sQ, w, lane);
       ++S.tile;
       stream_settle(S, p, cu, pos0, lane);
-      row_entry(nx, S, p, qd * 32 + lane);
+      row_entry(nx, S, p, myrow);
     };
     take();
     queries();
@@ -554,14 +548,14 @@ __global__ void __launch_bounds__(kLaunch, 1)
             ok = ok && tc::mbar_wait_hint(bar_pv + mb, (n - 1) & 1, p.err, kHintNs);
             tc::tc_fence_after();
           }
-          if (qd == 0 && lane == 0) {              // lane 0 of quarter 0: the tile's first row
+          if (w == 0 && lane == 0) {               // this lane's row is the tile's first
             tc::mbar_arrive_expect_tx(bar_full + mb, 2 * kKVBlk);
             tc::tma_load_2d(sKV + 2 * mb * kKVBlk, &tm_rows, 128 * mb, code, bar_full + mb);
             tc::tma_load_2d(sKV + (2 * mb + 1) * kKVBlk, &tm_rows, 128 * mb + 64, code, bar_full + mb);
           }
         }
         row_page(nx, S.it.seq, p);
-        if (lane == 0) s_valid[qd] = have;
+        if (lane == 0) s_valid16[w] = (uint16_t)have;
         if (wait_q) tc::cp_async_wait_all();
 #pragma unroll
         for (int mb = 0; mb < 4; ++mb) {
@@ -575,7 +569,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
         const bool fast = __all_sync(0xffffffffu, scales_fast(sc));
 #pragma unroll 1
         for (int mb = 0; mb < 4; ++mb) {
-          uint4 cv[8];
+          uint4 cv[4];
           if (fast) {
             if (mb < 3) convert_fp8<false>(st, sc, mb, 0, cv, lane);
             else convert_fp8<true>(st, sc, mb, 0, cv, lane);
@@ -585,7 +579,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
             tc::tc_fence_after();
           }
           if (!fast) {
-            move_fp8_slow(p, code, mb, sKV, row0 + lane);
+            move_fp8_slow(p, code, mb, sKV, myrow, lane >> 4);
           } else if (mb < 3) {
             store_fp8<false>(cv, mb, 0, sKV, row0, lane);
             convert_fp8<false>(st, sc, mb, 1, cv, lane);
@@ -595,13 +589,13 @@ __global__ void __launch_bounds__(kLaunch, 1)
             store_hi(st, sKV, row0, lane);
           }
           if (mb == 0) {
-            if (lane == 0) s_valid[qd] = have;
+            if (lane == 0) s_valid16[w] = (uint16_t)have;
             if (wait_q) tc::cp_async_wait_all();
           }
           pair_landed(mb);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) st[i] = st[i + 8];
-          if (mb == 1) load_fp8_last(st, c8, p, lane);
+          for (int i = 0; i < 8; ++i) st[i] = st[i + 4];
+          if (mb == 1) load_fp8_last(st, c4, p, lane);
           if (mb == 2) row_page(nx, S.it.seq, p);
         }
       } else {
@@ -613,11 +607,11 @@ __global__ void __launch_bounds__(kLaunch, 1)
           }
           store_bf16(st, mb, sKV, row0, lane);
           if (mb == 0) {
-            if (lane == 0) s_valid[qd] = have;
+            if (lane == 0) s_valid16[w] = (uint16_t)have;
             if (wait_q) tc::cp_async_wait_all();
           }
           pair_landed(mb);
-          if (mb < 2) load_bf16(st, mb + 2, rp);
+          if (mb < 2) load_bf16(st, mb + 2, p, window, c4, lane);
           if (mb == 2) row_page(nx, S.it.seq, p);
         }
       }
@@ -630,7 +624,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // ------------------------------------------------------------------ softmax and output
     const int qd = warp & 3, hf = warp >> 2;
     const int row = qd * 32 + lane;                // TMEM lane = tile row of this thread
