@@ -408,42 +408,65 @@ def _plain(dtype):
 
 
 _BYTES = (torch.uint8, torch.float8_e4m3fn)
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _arg(x, dtype, what, numel=None):
-    """Address of a contiguous CUDA tensor of the given type (and at least numel elements)
-    on the current device; None stays None."""
+def _place(stream):
+    """(current device, stream) of a call: torch's current stream there unless one is given."""
+    if not torch.cuda.is_initialized() and not torch.cuda.is_available():
+        raise CsaError("tensor arguments must be CUDA tensors, and there is no CUDA device")
+    dev = torch.cuda.current_device()
+    if stream is None:
+        return dev, _raw_stream(dev)
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
+        raise CsaError("the stream is on %s, not on the current device" % stream.device)
+    return dev, _stream(stream)
+
+
+def _bad(x, dtype, what, numel, dev):
+    if not x.is_cuda:
+        return "tensor arguments must be CUDA tensors (%s is on %s)" % (what, x.device)
+    if x.dtype is not dtype and not (dtype is torch.uint8 and x.dtype in _BYTES):
+        return "%s must be %s (got %s)" % (what, dtype, x.dtype)
+    if x.get_device() != dev:
+        return "%s is on %s, not on the current device" % (what, x.device)
+    if not x.is_contiguous():
+        return "%s must be contiguous" % what
+    if x.numel() < numel:
+        return "%s holds %d elements, %d are needed" % (what, x.numel(), numel)
+    return None
+
+
+def _arg(x, dtype, what, numel, dev):
+    """Address of a contiguous CUDA tensor of the given type and at least numel elements on
+    device dev; None stays None."""
     if x is None:
         return None
-    p = _ptr(x)
-    if x.dtype != dtype and not (dtype is torch.uint8 and x.dtype in _BYTES):
-        raise CsaError("%s must be %s (got %s)" % (what, dtype, x.dtype))
-    if x.device.index != torch.cuda.current_device():
-        raise CsaError("%s is on %s, not on the current device" % (what, x.device))
-    if numel is not None and x.numel() < numel:
-        raise CsaError("%s holds %d elements, %d are needed" % (what, x.numel(), numel))
-    return p
+    if (x.dtype is dtype and x.is_cuda and x.get_device() == dev and x.is_contiguous() and
+            x.numel() >= numel):
+        return x.data_ptr()
+    why = _bad(x, dtype, what, numel, dev)
+    if why:
+        raise CsaError(why)
+    return x.data_ptr()
 
 
-def _strided(x, dtype, n, rows, what):
-    """(address, elements between rows) of a CUDA tensor of `rows` rows of n elements whose
-    first dimension may be strided."""
+def _strided(x, dtype, n, rows, what, dev):
+    """(address, elements between rows) of a CUDA tensor of at least `rows` rows of n elements
+    whose first dimension may be strided."""
     if x is None:
         return None, 0
-    if x.device.type != "cuda":
-        raise CsaError("tensor arguments must be CUDA tensors (got %s)" % x.device)
-    if x.dtype != dtype:
-        raise CsaError("%s must be %s (got %s)" % (what, dtype, x.dtype))
-    if x.device.index != torch.cuda.current_device():
-        raise CsaError("%s is on %s, not on the current device" % (what, x.device))
+    if x.is_contiguous():
+        if x.dim() < 2 or x.shape[0] < rows or x.numel() != x.shape[0] * n:
+            raise CsaError("%s must hold %d rows of %d elements (got %s)" % (what, rows, n, tuple(x.shape)))
+        return _arg(x, dtype, what, 0, dev), n
     if x.dim() < 2 or x.shape[0] < rows or x.numel() != x.shape[0] * n:
-        raise CsaError("%s must hold %d rows of %d elements (got %s)" % (what, rows, n,
-                                                                     tuple(x.shape)))
-    step = 1
-    for size, stride in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
-        if size != 1 and stride != step:
-            raise CsaError("%s: the elements of a row must be contiguous" % what)
-        step *= size
+        raise CsaError("%s must hold %d rows of %d elements (got %s)" % (what, rows, n, tuple(x.shape)))
+    if not x[0].is_contiguous():
+        raise CsaError("%s: the elements of a row must be contiguous" % what)
+    why = _bad(x[0], dtype, what, 0, dev)
+    if why:
+        raise CsaError(why)
     # a single row has no distance to the next: torch may report any
     return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else n
 
@@ -464,11 +487,14 @@ def kv_cache(dtype, c, d_hi, rows, hi, scales, block_table):
     if dtype != CSA_FP8_E4M3 and (hi is not None or scales is not None):
         raise CsaError("hi and scales belong to an FP8 cache")
     stride = ((c - d_hi) // SCALE_GROUP + 7) // 8 * 8
+    dev = rows.get_device()
     kv = KVCache(dtype=dtype, c=c, d_hi=d_hi, num_pages=pages, max_pages=block_table.shape[1],
-                 rows=_arg(rows, _ELEM[dtype], "rows"), hi=_arg(hi, torch.bfloat16, "hi", n * d_hi),
-                 scales=_arg(scales, torch.uint8, "scales", n * stride),
-                 block_table=_arg(block_table, torch.int32, "block_table"))
+                 rows=_arg(rows, _ELEM[dtype], "rows", 0, dev),
+                 hi=_arg(hi, torch.bfloat16, "hi", n * d_hi, dev),
+                 scales=_arg(scales, torch.uint8, "scales", n * stride, dev),
+                 block_table=_arg(block_table, torch.int32, "block_table", 0, dev))
     kv._tensors = (rows, hi, scales, block_table)
+    kv._place = (dev, block_table.shape[0])
     return kv
 
 
@@ -484,44 +510,50 @@ def alloc_kv_cache(dtype, c, d_hi, num_pages, block_table, device="cuda"):
                     torch.zeros((n, stride), dtype=torch.uint8, device=device), block_table)
 
 
-def _kv(kv, b):
-    """The cache, whose block table must have a row for each of b sequences."""
-    if kv._tensors[3].shape[0] < b:
-        raise CsaError("block_table has %d rows for %d sequences" % (kv._tensors[3].shape[0], b))
+def _kv(kv, b, dev):
+    """The cache, on device dev, whose block table must have a row for each of b sequences."""
+    if kv._place[0] != dev:
+        raise CsaError("the cache is on device %d, not on the current one" % kv._place[0])
+    if kv._place[1] < b:
+        raise CsaError("block_table has %d rows for %d sequences" % (kv._place[1], b))
     return ctypes.byref(kv)
 
 
 def csa_cache_write(kv, x_dtype, x, cu_rows, first, b, rows, stream=None):
     """x: [rows][c], rows possibly strided (a slice of a wider tensor)."""
-    p, stride = _strided(x, _plain(x_dtype), kv.c, rows, "x")
-    _check(lib().csa_cache_write(_kv(kv, b), x_dtype, p, stride,
-                                 _arg(cu_rows, torch.int32, "cu_rows", b + 1),
-                                 _arg(first, torch.int32, "first", b), b, rows, _stream(stream)))
+    dev, st = _place(stream)
+    p, stride = _strided(x, _plain(x_dtype), kv.c, rows, "x", dev)
+    _check(lib().csa_cache_write(_kv(kv, b, dev), x_dtype, p, stride,
+                                 _arg(cu_rows, torch.int32, "cu_rows", b + 1, dev),
+                                 _arg(first, torch.int32, "first", b, dev), b, rows, st))
 
 
 def csa_cache_read(kv, idx, count, b, k, out_dtype, out, stream=None):
-    _check(lib().csa_cache_read(_kv(kv, b), _arg(idx, torch.int32, "idx", b * k),
-                                _arg(count, torch.int32, "count", b), b, k, out_dtype,
-                                _arg(out, _plain(out_dtype), "out", b * k * kv.c), _stream(stream)))
+    dev, st = _place(stream)
+    _check(lib().csa_cache_read(_kv(kv, b, dev), _arg(idx, torch.int32, "idx", b * k, dev),
+                                _arg(count, torch.int32, "count", b, dev), b, k, out_dtype,
+                                _arg(out, _plain(out_dtype), "out", b * k * kv.c, dev), st))
 
 
 def csa_window_append(dtype, c, n_w, win, x, cu_rows, first, b, rows, stream=None):
-    p, stride = _strided(x, _plain(dtype), c, rows, "x")
-    _check(lib().csa_window_append(dtype, c, n_w, _arg(win, _plain(dtype), "win", b * n_w * c), p,
-                                   stride, _arg(cu_rows, torch.int32, "cu_rows", b + 1),
-                                   _arg(first, torch.int32, "first", b), b, rows, _stream(stream)))
+    dev, st = _place(stream)
+    p, stride = _strided(x, _plain(dtype), c, rows, "x", dev)
+    _check(lib().csa_window_append(dtype, c, n_w, _arg(win, _plain(dtype), "win", b * n_w * c, dev), p,
+                                   stride, _arg(cu_rows, torch.int32, "cu_rows", b + 1, dev),
+                                   _arg(first, torch.int32, "first", b, dev), b, rows, st))
 
 
 def csa_qk_norm_rope(p, q, q_gain, kv, kv_gain, pos, N, q_out, kv_out, stream=None):
     """q: [N][H][d] and kv: [N][d], tokens possibly strided; either may be None."""
-    dt = _plain(p.dtype)
-    qp, qs = _strided(q, dt, p.H * p.d, N, "q")
-    kp, ks = _strided(kv, dt, p.d, N, "kv")
-    _check(lib().csa_qk_norm_rope(ctypes.byref(p), qp, qs, _arg(q_gain, torch.float32, "q_gain", p.d),
-                                  kp, ks, _arg(kv_gain, torch.float32, "kv_gain", p.d),
-                                  _arg(pos, torch.int32, "pos", N), N,
-                                  _arg(q_out, dt, "q_out", N * p.H * p.d),
-                                  _arg(kv_out, dt, "kv_out", N * p.d), _stream(stream)))
+    dev, st = _place(stream)
+    dt, d = _plain(p.dtype), p.d
+    qp, qs = _strided(q, dt, p.H * d, N, "q", dev)
+    kp, ks = _strided(kv, dt, d, N, "kv", dev)
+    _check(lib().csa_qk_norm_rope(ctypes.byref(p), qp, qs, _arg(q_gain, torch.float32, "q_gain", d, dev),
+                                  kp, ks, _arg(kv_gain, torch.float32, "kv_gain", d, dev),
+                                  _arg(pos, torch.int32, "pos", N, dev), N,
+                                  _arg(q_out, dt, "q_out", N * p.H * d, dev),
+                                  _arg(kv_out, dt, "kv_out", N * d, dev), st))
 
 
 def csa_chunk_attn_workspace_size(p, kv, b, N, L_max):
@@ -534,17 +566,17 @@ def csa_chunk_attn_launch_count(p, kv, b, N, L_max):
 
 def csa_chunk_attn(p, kv, q, cu_q, pos0, idx, count, win, new_win, sink, b, N, L_max, out, lse=None,
                    ws=None, ws_bytes=None, stream=None):
-    dt = _plain(p.dtype)
+    dev, st = _place(stream)
+    dt, d = _plain(p.dtype), p.d
     if ws_bytes is None:
-        ws_bytes = ws.numel() * ws.element_size() if isinstance(ws, torch.Tensor) else 0
-    n = N * p.H * p.d
-    _check(lib().csa_chunk_attn(ctypes.byref(p), _kv(kv, b), _arg(q, dt, "q", n),
-                                _arg(cu_q, torch.int32, "cu_q", b + 1),
-                                _arg(pos0, torch.int32, "pos0", b),
-                                _arg(idx, torch.int32, "idx", N * p.k),
-                                _arg(count, torch.int32, "count", N),
-                                _arg(win, dt, "win", b * p.n_w * p.d),
-                                _arg(new_win, dt, "new_win", N * p.d),
-                                _arg(sink, torch.float32, "sink", p.H), b, N, L_max,
-                                _arg(out, dt, "out", n), _arg(lse, torch.float32, "lse", N * p.H),
-                                _ptr(ws), ws_bytes, _stream(stream)))
+        ws_bytes = ws.numel() * ws.element_size() if ws is not None else 0
+    n = N * p.H * d
+    i32, f32 = torch.int32, torch.float32
+    _check(lib().csa_chunk_attn(ctypes.byref(p), _kv(kv, b, dev), _arg(q, dt, "q", n, dev),
+                                _arg(cu_q, i32, "cu_q", b + 1, dev), _arg(pos0, i32, "pos0", b, dev),
+                                _arg(idx, i32, "idx", N * p.k, dev), _arg(count, i32, "count", N, dev),
+                                _arg(win, dt, "win", b * p.n_w * d, dev),
+                                _arg(new_win, dt, "new_win", N * d, dev),
+                                _arg(sink, f32, "sink", p.H, dev), b, N, L_max,
+                                _arg(out, dt, "out", n, dev), _arg(lse, f32, "lse", N * p.H, dev),
+                                _arg(ws, ws.dtype if ws is not None else None, "ws", 0, dev), ws_bytes, st))
