@@ -10,8 +10,10 @@
 // Memory bound: a quantised row of 512 dims is 584 bytes (448 codes, 64 bf16 dims, 7 scale
 // exponents) against 1024 in bf16.  A warp owns a row: lane l takes 16 consecutive dims, so
 // 512 dims are one pass of the warp, a scale group is four neighbouring lanes (two shuffles
-// for its maximum) and codes leave as 16-byte stores.  Large calls take several rows per
-// warp with every row's loads issued before the first is used.
+// for its maximum) and codes leave as 16-byte stores.  Large calls take two rows per warp,
+// both loaded before the first is used, with registers held to five CTAs an SM.  262,144 rows
+// of 512 (421 MB): written 78 us, read back 79 us, 5.4 TB/s (four rows per warp 82 and 87 us,
+// one 82 and 99); 16 rows 2.3 us, a selection of 16 x 512 rows 4.9 us.
 #include "chunk_common.cuh"
 
 namespace csa {
@@ -88,18 +90,29 @@ __device__ __forceinline__ int scale_exp(float amax) {
   return max(kScaleExpMin, min(k, kScaleExpMax));
 }
 
-// Row r of the ragged rows -> its row in the pool, or -1 (whole warp).
-__device__ __forceinline__ long long dest_row(const csa_kv_cache& kv, const RowsArgs& a, int r,
-                                              int lane) {
-  if (r >= a.rows) return -1;
-  const int s = find_seq(a.cu, a.b, r, lane);
-  if (s >= a.b || r < a.cu[s]) return -1;
-  return page_row(kv, s, (long long)a.first[s] + (r - a.cu[s]));
+// Rows r0 .. r0 + R - 1 of the ragged rows -> their rows in the pool, or -1 (whole warp).
+// Neighbouring rows mostly share a sequence, so the search runs for the first alone.
+template <int R>
+__device__ __forceinline__ void dest_rows(long long (&at)[R], const csa_kv_cache& kv, const RowsArgs& a,
+                                          int r0, int lane) {
+  int s = find_seq(a.cu, a.b, r0, lane);
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int r = r0 + i;
+    while (s < a.b && r >= a.cu[s + 1]) ++s;
+    at[i] = r >= a.rows || s >= a.b || r < a.cu[s]
+                ? -1 : page_row(kv, s, (long long)a.first[s] + (r - a.cu[s]));
+  }
+}
+__device__ __forceinline__ long long dest_row(const csa_kv_cache& kv, const RowsArgs& a, int r, int lane) {
+  long long at[1];
+  dest_rows(at, kv, a, r, lane);
+  return at[0];
 }
 
 // FP8 rows.  T: type of x.  R: rows per warp.
 template <typename T, int R>
-__global__ void __launch_bounds__(32 * kLcWarps) write_fp8_kernel(csa_kv_cache kv, RowsArgs a) {
+__global__ void __launch_bounds__(32 * kLcWarps, 5) write_fp8_kernel(csa_kv_cache kv, RowsArgs a) {
   const int lane = threadIdx.x & 31;
   const int r0 = (blockIdx.x * kLcWarps + (threadIdx.x >> 5)) * R;
   if (r0 >= a.rows) return;
@@ -107,17 +120,16 @@ __global__ void __launch_bounds__(32 * kLcWarps) write_fp8_kernel(csa_kv_cache k
   uint8_t* codes = static_cast<uint8_t*>(kv.rows);
   __nv_bfloat16* hi = static_cast<__nv_bfloat16*>(kv.hi);
   uint8_t* scales = static_cast<uint8_t*>(kv.scales);
+  long long at[R];
   // c <= 512 is one pass; wider rows take the next 512 dims in another
   for (int c0 = 0; c0 < kv.c; c0 += 512) {
     const int ch = c0 + 16 * lane;
     Run16<T> x[R];
-    long long at[R];
 #pragma unroll
     for (int i = 0; i < R; ++i)   // the row's values do not depend on where it goes
       if (r0 + i < a.rows && ch < kv.c)
         x[i].load(reinterpret_cast<const T*>(a.x) + (long long)(r0 + i) * a.x_stride + ch);
-#pragma unroll
-    for (int i = 0; i < R; ++i) at[i] = dest_row(kv, a, r0 + i, lane);
+    if (c0 == 0) dest_rows(at, kv, a, r0, lane);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (at[i] < 0) continue;    // uniform over the warp
@@ -195,7 +207,7 @@ __device__ __forceinline__ long long slot_row(const csa_kv_cache& kv, const int3
 }
 
 template <typename U, int R>
-__global__ void __launch_bounds__(32 * kLcWarps) read_fp8_kernel(csa_kv_cache kv, const int32_t* idx,
+__global__ void __launch_bounds__(32 * kLcWarps, 5) read_fp8_kernel(csa_kv_cache kv, const int32_t* idx,
                                                                  const int32_t* count, int k,
                                                                  long long slots, U* out) {
   const int lane = threadIdx.x & 31;
@@ -274,14 +286,14 @@ inline unsigned blocks(long long rows, int per_warp) {
   return (unsigned)((rows + (long long)kLcWarps * per_warp - 1) / ((long long)kLcWarps * per_warp));
 }
 
-// Rows enough that four per warp still give every SM its 64 warps.
+// Rows enough that two per warp still give every SM a few waves of warps.
 inline bool many(long long rows) { return rows >= 148LL * 64 * 4; }
 
 template <typename T>
 void write_t(const csa_kv_cache& kv, const RowsArgs& a, cudaStream_t st) {
   const int thr = 32 * kLcWarps;
   if (kv.dtype == CSA_FP8_E4M3) {
-    constexpr int R = sizeof(T) == 2 ? 4 : 2;
+    constexpr int R = 2;
     if (many(a.rows)) write_fp8_kernel<T, R><<<blocks(a.rows, R), thr, 0, st>>>(kv, a);
     else write_fp8_kernel<T, 1><<<blocks(a.rows, 1), thr, 0, st>>>(kv, a);
   } else if (kv.dtype == CSA_BF16) {
@@ -296,7 +308,7 @@ void read_t(const csa_kv_cache& kv, const int32_t* idx, const int32_t* count, in
             long long slots, U* out, cudaStream_t st) {
   const int thr = 32 * kLcWarps;
   if (kv.dtype == CSA_FP8_E4M3) {
-    if (many(slots)) read_fp8_kernel<U, 4><<<blocks(slots, 4), thr, 0, st>>>(kv, idx, count, k, slots, out);
+    if (many(slots)) read_fp8_kernel<U, 2><<<blocks(slots, 2), thr, 0, st>>>(kv, idx, count, k, slots, out);
     else read_fp8_kernel<U, 1><<<blocks(slots, 1), thr, 0, st>>>(kv, idx, count, k, slots, out);
   } else if (kv.dtype == CSA_BF16) {
     read_plain_kernel<__nv_bfloat16, U><<<blocks(slots, 1), thr, 0, st>>>(kv, idx, count, k, slots, out);
