@@ -37,7 +37,6 @@
 // row), run two tiles ahead of their use.
 #include "chunk_common.cuh"
 #include "tc_common.cuh"
-#include "xpose.cuh"
 
 #include <algorithm>
 #include <climits>
@@ -367,6 +366,22 @@ __device__ __forceinline__ void pair_landed(int mb) {
   tc::named_bar_arrive(4 + mb, kBarP);
 }
 
+// 16 TMEM lanes x 32 columns: lane l gets TMEM lanes l / 4 and l / 4 + 8, columns 8 g + 2 (l % 4) and the next, as
+// r[4 g], r[4 g + 1] and r[4 g + 2], r[4 g + 3].
+__device__ __forceinline__ void tmem_ld16(uint32_t ta, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(ta) : "memory");
+  asm volatile(
+      "tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+      :: "memory");
+}
+
 // The query heads of a token into shared memory (cp.async, by the producer warps).
 __device__ __forceinline__ void load_q(const ChunkTc& p, int tok, uint8_t* sQ, int warp, int lane) {
   const __nv_bfloat16* qb = p.q + (long long)tok * kH * kD;
@@ -397,11 +412,9 @@ __global__ void __launch_bounds__(kLaunch, 1)
   uint8_t* sP = sQ + 8 * kQBlk;                   // 16 KB
   float* s_red = reinterpret_cast<float*>(sP + kRows * 128);   // [4][64]
   float* s_M = s_red + 4 * kH;                    // running reference maximum, log2 units
-  float* s_Mu = s_M + kH;                         // the same, 0 where it is -inf
-  float* s_alpha = s_Mu + kH;
+  float* s_alpha = s_M + kH;
   float* s_sink2 = s_alpha + kH;
-  float* s_zero = s_sink2 + kH;
-  int* s_flag = reinterpret_cast<int*>(s_zero + kH);
+  int* s_flag = reinterpret_cast<int*>(s_sink2 + kH);
   uint64_t* bar_s = reinterpret_cast<uint64_t*>(s_flag + 4);
   uint64_t* bar_pv = bar_s + 1;                   // [4]
   uint64_t* bar_full = bar_pv + 4;                // [4]: a pair's TMA copies have landed
@@ -420,7 +433,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
   }
   const int32_t* cu = cached ? s_cu : p.cu_q;
   const int32_t* pos0 = cached ? s_pos0 : p.pos0;
-  if (tid < kH) { s_sink2[tid] = p.sink[tid] * kLog2e; s_zero[tid] = 0.f; }
+  if (tid < kH) s_sink2[tid] = p.sink[tid] * kLog2e;
   if (tid == 0) {
     tc::mbar_init(bar_s, 1);
     for (int i = 0; i < 8; ++i) tc::mbar_init(bar_pv + i, 1);
@@ -443,8 +456,6 @@ __global__ void __launch_bounds__(kLaunch, 1)
     const uint64_t dS_b = tc::smem_desc_sw128(tc::smem_u32(sQ), 16, 1024);
     const uint64_t dO_a = tc::smem_desc_sw128(tc::smem_u32(sKV), kKVBlk, 1024);
     const uint64_t dO_b = tc::smem_desc_sw128(tc::smem_u32(sP), 8192, 1024);
-    const uint32_t uS = __shfl_sync(0xffffffffu, tS, 0), uO = uS + 64;
-    const uint32_t el = tc::elect_one();
     for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
       const Item I = get_item(p, cu, pos0, item, lane);
       if (!I.live) break;
@@ -453,26 +464,32 @@ __global__ void __launch_bounds__(kLaunch, 1)
         for (int mb = 0; mb < 4; ++mb) {
           tc::named_bar(4 + mb, kBarP);             // the pair (and, with the first, q) is in place
           tc::tc_fence_after();
+          if (tc::elect_one()) {
+            const uint64_t a0 = tc::desc_advance(dS_a, 2 * mb * kKVBlk), b0 = tc::desc_advance(dS_b, 2 * mb * kQBlk);
 #pragma unroll
-          for (int kb = 0; kb < 2; ++kb) {
+            for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc::mma_f16_el(uS, tc::desc_advance(dS_a, (2 * mb + kb) * kKVBlk + kk * 32),
-                             tc::desc_advance(dS_b, (2 * mb + kb) * kQBlk + kk * 32), idS, (mb | kb | kk) != 0,
-                             el);
+              for (int kk = 0; kk < 4; ++kk)
+                tc::mma_f16(tS, tc::desc_advance(a0, kb * kKVBlk + kk * 32),
+                            tc::desc_advance(b0, kb * kQBlk + kk * 32), idS, (mb | kb | kk) != 0);
+            }
+            if (mb == 3) tc::mma_commit(bar_s);
           }
+          __syncwarp();
         }
-        if (el) tc::mma_commit(bar_s);
         __syncwarp();
         tc::named_bar(2, kBarS);                    // P^T in place, O^T rescaled
         tc::tc_fence_after();
 #pragma unroll 1
         for (int mb = 0; mb < 4; ++mb) {
+          if (tc::elect_one()) {
+            const uint64_t a0 = tc::desc_advance(dO_a, 2 * mb * kKVBlk);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc::mma_f16_el(uO + mb * kH, tc::desc_advance(dO_a, 2 * mb * kKVBlk + kk * 2048),
-                           tc::desc_advance(dO_b, kk * 2048), idO, (kk > 0) || (j > I.tb), el);
-          if (el) tc::mma_commit(bar_pv + mb);     // column blocks 2 mb, 2 mb + 1 are free
+            for (int kk = 0; kk < 8; ++kk)
+              tc::mma_f16(tO + mb * kH, tc::desc_advance(a0, kk * 2048), tc::desc_advance(dO_b, kk * 2048), idO,
+                          (kk > 0) || (j > I.tb));
+            tc::mma_commit(bar_pv + mb);           // column blocks 2 mb, 2 mb + 1 are free
+          }
           __syncwarp();
         }
       }
@@ -627,8 +644,10 @@ __global__ void __launch_bounds__(kLaunch, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // ------------------------------------------------------------------ softmax and output
     const int qd = warp & 3, hf = warp >> 2;
-    const int row = qd * 32 + lane;                // TMEM lane = tile row of this thread
     const uint32_t lane_addr = (uint32_t)(qd * 32) << 16;
+    const int r0 = 32 * qd + (lane >> 2);          // this thread's rows of S^T: r0 + 8 y, y < 4
+    const int h0 = 32 * hf + 2 * (lane & 3);       // ... and heads h0 + 8 g, h0 + 8 g + 1, g < 4
+    const int row = qd * 32 + lane;                // its TMEM lane of O^T
     uint32_t ns = 0;                               // tiles so far
     bool ok = true;
 
@@ -636,81 +655,87 @@ __global__ void __launch_bounds__(kLaunch, 1)
       const Item I = get_item(p, cu, pos0, item, lane);
       if (!I.live) break;
       bool started = false;                        // a tile of this item had a row
-      float lsum[32];
+      float lsum[8], ref[8];                       // sums, and reference maxima (log2 units, 0: none)
 #pragma unroll
-      for (int h = 0; h < 32; ++h) lsum[h] = 0.f;
+      for (int h = 0; h < 8; ++h) lsum[h] = ref[h] = 0.f;
       for (int j = I.tb; j < I.te; ++j) {
         ok = ok && tc::mbar_wait_hint(bar_s, ns & 1, p.err, kHintNs);
         ++ns;
         tc::tc_fence_after();
         const uint32_t have = s_valid[qd];
-        const bool valid = (have >> lane) & 1u;
-        const bool full = have == 0xffffffffu;
-        // logits less the running maximum, log2 units
-        uint32_t lg[32];
-        auto logits = [&](const float* ref) {
-          tc::tmem_ld32(tS + lane_addr + 32 * hf, lg);
-          tc::tmem_ld_wait(lg);
+        // logits less the reference, log2 units
+        // (lg[y]: rows r0 + 16 y, 8 further)
+        uint32_t lg[2][16];
+        auto logits = [&]() {
 #pragma unroll
-          for (int h = 0; h < 32; h += 4) {
-            const float4 M4 = *reinterpret_cast<const float4*>(ref + 32 * hf + h);
-            lg[h] = __float_as_uint(fmaf(__uint_as_float(lg[h]), p.scale_log2, -M4.x));
-            lg[h + 1] = __float_as_uint(fmaf(__uint_as_float(lg[h + 1]), p.scale_log2, -M4.y));
-            lg[h + 2] = __float_as_uint(fmaf(__uint_as_float(lg[h + 2]), p.scale_log2, -M4.z));
-            lg[h + 3] = __float_as_uint(fmaf(__uint_as_float(lg[h + 3]), p.scale_log2, -M4.w));
-            if (h % 8 == 4) asm volatile("" ::: "memory");   // not all references in registers at once
+          for (int y = 0; y < 2; ++y) tmem_ld16(tS + lane_addr + ((uint32_t)(16 * y) << 16) + 32 * hf, lg[y]);
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              lg[y][i] = __float_as_uint(fmaf(__uint_as_float(lg[y][i]), p.scale_log2, -ref[2 * (i >> 2) + (i & 1)]));
           }
-          if (!full) {
+          if (have != 0xffffffffu) {
+            const uint32_t v = have >> (lane >> 2);
 #pragma unroll
-            for (int h = 0; h < 32; ++h)
-              if (!valid) lg[h] = __float_as_uint(-INFINITY);
+            for (int y = 0; y < 2; ++y) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (!((v >> (16 * y + 4 * (i & 2))) & 1u)) lg[y][i] = __float_as_uint(-INFINITY);
+            }
           }
         };
+        logits();
         // the item's first tile, and any up to the first with a row, set the maximum
         bool exact = !started;
-        logits(exact ? s_zero : s_Mu);
         if (!exact) {
           float top = -INFINITY;
 #pragma unroll
-          for (int h = 0; h < 32; ++h) top = fmaxf(top, __uint_as_float(lg[h]));
+          for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(lg[i >> 4][i & 15]));
           exact = tc::bar_red_or(3, kST, top > kRescale);
         }
         if (exact) {
-          // the reduction consumes the logits, which are read from TMEM again below (keeping
-          // them beside it would not fit the registers)
-          {
-            float v[32];
+          float v[8];
 #pragma unroll
-            for (int h = 0; h < 32; ++h) v[h] = __uint_as_float(lg[h]);
-            xpose_reduce32<true>(v, lane);
-            if (tid == 0) s_flag[0] = 0;           // its last reads are behind two barriers
-            s_red[qd * kH + 32 * hf + lane] = v[0];
+          for (int g = 0; g < 4; ++g) {
+            v[2 * g] = v[2 * g + 1] = -INFINITY;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              v[2 * g] = fmaxf(v[2 * g], fmaxf(__uint_as_float(lg[y][4 * g]), __uint_as_float(lg[y][4 * g + 2])));
+              v[2 * g + 1] = fmaxf(v[2 * g + 1], fmaxf(__uint_as_float(lg[y][4 * g + 1]), __uint_as_float(lg[y][4 * g + 3])));
+            }
+          }
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+#pragma unroll
+            for (int h = 0; h < 8; ++h) v[h] = fmaxf(v[h], __shfl_xor_sync(0xffffffffu, v[h], o));
+          }
+          if (tid == 0) s_flag[0] = 0;             // its last reads are behind a barrier
+          if (lane < 4) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              *reinterpret_cast<float2*>(s_red + qd * kH + h0 + 8 * g) = make_float2(v[2 * g], v[2 * g + 1]);
           }
           tc::named_bar(3, kST);
           if (tid < kH) {
             // this tile's maxima, relative to the reference that the logits were taken against
             const float tm = fmaxf(fmaxf(s_red[tid], s_red[kH + tid]), fmaxf(s_red[2 * kH + tid], s_red[3 * kH + tid]));
-            const float Mr = s_M[tid];
-            float Mn = Mr, al = 1.f;
-            if (!started) {
-              Mn = tm;
-              al = 0.f;                            // O^T, if any, is zero so far
-            } else if (tm > kRescale) {
-              Mn = Mr + tm;
+            float Mn = started ? s_M[tid] : tm, al = started ? 1.f : 0.f;
+            if (started && tm > kRescale) {
+              Mn += tm;
               al = exp2f(-tm);
               s_flag[0] = 1;
             }
             s_M[tid] = Mn;
-            s_Mu[tid] = Mn == -INFINITY ? 0.f : Mn;   // a tile without rows gives p = 0, not NaN
             s_alpha[tid] = al;
           }
           tc::named_bar(3, kST);
           if (started && s_flag[0]) {
 #pragma unroll 1
-            for (int x = 0; x < 4; ++x) {          // this half's two dim blocks, 32 heads each time
+            for (int y = 0; y < 4; ++y) {          // this half's two dim blocks, 32 heads each time
               uint32_t o[32];
-              const uint32_t ta = tO + 2 * hf * kH + x * 32 + lane_addr;
-              const float* al = s_alpha + 32 * (x & 1);
+              const uint32_t ta = tO + 2 * hf * kH + y * 32 + lane_addr;
+              const float* al = s_alpha + 32 * (y & 1);
               tc::tmem_ld32(ta, o);
               tc::tmem_ld_wait(o);
 #pragma unroll
@@ -721,27 +746,37 @@ __global__ void __launch_bounds__(kLaunch, 1)
               tc::tmem_st32(ta, o);
             }
             tc::tmem_st_wait();
+          }
 #pragma unroll
-            for (int h = 0; h < 32; ++h) lsum[h] *= s_alpha[32 * hf + h];
+          for (int g = 0; g < 4; ++g) {
+            const float2 M2 = *reinterpret_cast<const float2*>(s_M + h0 + 8 * g);
+            const float2 a2 = *reinterpret_cast<const float2*>(s_alpha + h0 + 8 * g);
+            ref[2 * g] = M2.x == -INFINITY ? 0.f : M2.x;   // a tile without rows gives p = 0, not NaN
+            ref[2 * g + 1] = M2.y == -INFINITY ? 0.f : M2.y;
+            lsum[2 * g] *= a2.x;
+            lsum[2 * g + 1] *= a2.y;
           }
           started = s_M[0] != -INFINITY;           // rows are masked for all heads alike
-          logits(s_Mu);
+          logits();
+          // nobody may overwrite these maxima before everyone has read them
+          tc::named_bar(3, kST);
         }
-        // probabilities: bf16 into P^T (this row's 128-byte line, four 16-byte chunks of it);
-        // the sums take them before that rounding
+        // probabilities: bf16 into P^T (a row's 128-byte line of 64 heads); the sums take them
+        // before that rounding
 #pragma unroll
-        for (int cb = 0; cb < 4; ++cb) {
-          uint32_t w4[4];
+        for (int y = 0; y < 2; ++y) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int h = cb * 8 + 2 * e;
-            const float p0 = ex2(__uint_as_float(lg[h])), p1 = ex2(__uint_as_float(lg[h + 1]));
-            lsum[h] += p0;
-            lsum[h + 1] += p1;
-            const __nv_bfloat162 a = __floats2bfloat162_rn(p0, p1);
-            w4[e] = *reinterpret_cast<const uint32_t*>(&a);
+          for (int g = 0; g < 4; ++g) {
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              const float p0 = ex2(__uint_as_float(lg[y][4 * g + e])), p1 = ex2(__uint_as_float(lg[y][4 * g + e + 1]));
+              lsum[2 * g] += p0;
+              lsum[2 * g + 1] += p1;
+              const int r = r0 + 16 * y + 4 * e;   // e = 2: the row eight further
+              *reinterpret_cast<__nv_bfloat162*>(sP + r * 128 + (((4 * hf + g) ^ (r & 7)) << 4) + 4 * (lane & 3)) =
+                  __floats2bfloat162_rn(p0, p1);
+            }
           }
-          sts16(sP + row * 128 + (((4 * hf + cb) ^ (row & 7)) << 4), w4[0], w4[1], w4[2], w4[3]);
         }
         tc::fence_proxy_async();
         tc::tc_fence_before();
@@ -762,9 +797,17 @@ __global__ void __launch_bounds__(kLaunch, 1)
         }
         continue;
       }
-      xpose_reduce32<false>(lsum, lane);
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+#pragma unroll
+        for (int h = 0; h < 8; ++h) lsum[h] += __shfl_xor_sync(0xffffffffu, lsum[h], o);
+      }
       tc::named_bar(3, kST);                       // s_red's readers of the last maximum are done
-      s_red[qd * kH + 32 * hf + lane] = lsum[0];
+      if (lane < 4) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<float2*>(s_red + qd * kH + h0 + 8 * g) = make_float2(lsum[2 * g], lsum[2 * g + 1]);
+      }
       tc::named_bar(3, kST);
       if (tid < kH) {
         const float l = s_red[tid] + s_red[kH + tid] + s_red[2 * kH + tid] + s_red[3 * kH + tid];
@@ -899,7 +942,7 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(ChunkTc p) {
   *reinterpret_cast<uint2*>(p.out + ((long long)tok * kH + h) * kD + d) = v;
 }
 
-constexpr size_t kSmem = 1024 + 8 * kKVBlk + 8 * kQBlk + kRows * 128 + (4 * kH + 5 * kH) * 4 + 16 + 9 * 8 + 8 + 16 +
+constexpr size_t kSmem = 1024 + 8 * kKVBlk + 8 * kQBlk + kRows * 128 + (4 * kH + 3 * kH) * 4 + 16 + 9 * 8 + 8 + 16 +
                          (2 * kSeqCache + 1) * 4;
 static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 

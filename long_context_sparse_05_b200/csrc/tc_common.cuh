@@ -180,17 +180,11 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a, uint64_t b,
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
       ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
 }
-// The same, issued by the one lane of a converged warp whose `el` is set (see elect_one): the
-// warp's code around it stays uniform, so descriptors live in uniform registers (a branch
-// around the instruction makes the compiler move them there for each one, ~25 cycles more).
-__device__ __forceinline__ void mma_f16_el(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
-                                           uint32_t accumulate, uint32_t el) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(el) : "memory");
-}
-// 1 in one lane of the (converged) warp, 0 in the others.
+// 1 in one lane of the (converged) warp, 0 in the others.  A branch on it is what the compiler
+// knows as "one thread of the warp": descriptors computed inside stay in uniform registers
+// (an M = 64, N = 64 MMA issues every 33 cycles, the rate it executes at; behind a branch on
+// the lane number or a predicate on the instruction, every 48 to 60, in a kernel short of
+// registers every 70 to 110).
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t r;
   asm volatile(
