@@ -28,7 +28,8 @@
 // barrier (the OR of "some logit exceeds the maximum") before its probabilities.
 //
 // CTA: warps 0-7 softmax and output (two per TMEM lane quarter, 32 heads each), warps 8-15
-// producers, warp 16 issues every MMA (17-19 idle: register shares go by warpgroup).
+// producers, warp 16 issues every MMA, told by warp 17 when a pair has landed (18-19 idle:
+// register shares go by warpgroup).
 // Producers walk the CTA's tiles as one stream across its items.
 //
 // Work item = (token, split of its tiles); CTAs walk the items with stride gridDim.x.  Few
@@ -60,7 +61,7 @@ constexpr int kSW = 8;                // softmax warps
 constexpr int kPW = 8;                // producer warps, each 16 of a tile's rows
 constexpr int kST = 32 * kSW;
 constexpr int kBarS = kST + 32;       // threads of a barrier of the softmax and the MMA warp
-constexpr int kBarP = 32 * kPW + 32;  // ... of the producers and the MMA warp
+constexpr int kBarW = 64;             // ... of the watching and the MMA warp
 constexpr int kLaunch = 640;
 // Registers a thread by warpgroup (2 x softmax, 2 x producers, MMA), out of 5 x 96 at launch.
 constexpr int kRegsSoftmax = 96, kRegsProd = 128, kRegsMma = 32;
@@ -358,12 +359,13 @@ __device__ __forceinline__ void move_fp8_slow(const ChunkTc& p, int code, int mb
   }
 }
 
-// This thread's part of a pair is in shared memory: publish it to the tensor core and arrive
-// at the pair's barrier (the MMA warp waits there).
-__device__ __forceinline__ void pair_landed(int mb) {
+// This warp's part of a pair is in shared memory: publish it (every lane its own writes) and
+// arrive once for the warp.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   tc::fence_proxy_async();
   tc::tc_fence_before();
-  tc::named_bar_arrive(4 + mb, kBarP);
+  __syncwarp();
+  if (lane == 0) tc::mbar_arrive(bar);
 }
 
 // 16 TMEM lanes x 32 columns: lane l gets TMEM lanes l / 4 and l / 4 + 8, columns 8 g + 2 (l % 4) and the next, as
@@ -417,7 +419,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
   int* s_flag = reinterpret_cast<int*>(s_sink2 + kH);
   uint64_t* bar_s = reinterpret_cast<uint64_t*>(s_flag + 4);
   uint64_t* bar_pv = bar_s + 1;                   // [4]
-  uint64_t* bar_full = bar_pv + 4;                // [4]: a pair's TMA copies have landed
+  uint64_t* bar_full = bar_pv + 4;                // [4]: a pair of the tile is in place
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bar_full + 4);
   uint32_t* s_valid = tmem_holder + 2;            // [4] the tile's rows that exist, a bit each
   uint16_t* s_valid16 = reinterpret_cast<uint16_t*>(s_valid);   // ... as the producers write them
@@ -436,7 +438,8 @@ __global__ void __launch_bounds__(kLaunch, 1)
   if (tid < kH) s_sink2[tid] = p.sink[tid] * kLog2e;
   if (tid == 0) {
     tc::mbar_init(bar_s, 1);
-    for (int i = 0; i < 8; ++i) tc::mbar_init(bar_pv + i, 1);
+    for (int i = 0; i < 4; ++i) tc::mbar_init(bar_pv + i, 1);
+    for (int i = 0; i < 4; ++i) tc::mbar_init(bar_full + i, kPW);
     tc::fence_barrier_init();
   }
   if (warp == 0) tc::tmem_alloc(tmem_holder, 512);
@@ -462,7 +465,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
       for (int j = I.tb; j < I.te; ++j) {
 #pragma unroll 1
         for (int mb = 0; mb < 4; ++mb) {
-          tc::named_bar(4 + mb, kBarP);             // the pair (and, with the first, q) is in place
+          tc::named_bar(4 + mb, kBarW);             // the pair (and, with the first, q) is in place
           tc::tc_fence_after();
           if (tc::elect_one()) {
             const uint64_t a0 = tc::desc_advance(dS_a, 2 * mb * kKVBlk), b0 = tc::desc_advance(dS_b, 2 * mb * kQBlk);
@@ -494,6 +497,24 @@ __global__ void __launch_bounds__(kLaunch, 1)
         }
       }
     }
+    }
+    // A poll of a barrier by the MMA warp itself would wait for the tensor pipe to drain, so a
+    // second warp watches the pairs land and hands each over at a named barrier.  (It cannot
+    // run ahead: a pair of the next tile lands after this tile's PV has read its place.)
+    if (warp == kSW + kPW + 1) {
+      bool ok = true;
+      uint32_t n = 0;
+      for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
+        const Item I = get_item(p, cu, pos0, item, lane);
+        if (!I.live) break;
+        for (int j = I.tb; j < I.te; ++j, ++n) {
+#pragma unroll 1
+          for (int mb = 0; mb < 4; ++mb) {
+            ok = ok && tc::mbar_wait_hint(bar_full + mb, n & 1, p.err, kHintNs);
+            tc::named_bar_arrive(4 + mb, kBarW);
+          }
+        }
+      }
     }
   } else if (warp >= kSW) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsProd));
@@ -555,7 +576,6 @@ __global__ void __launch_bounds__(kLaunch, 1)
     };
     take();
     queries();
-    uint32_t n_tma = 0;                            // tiles brought by TMA
     for (uint32_t n = 0; live; ++n) {
       const bool wait_q = new_q;
       if (!FP8 && whole) {
@@ -565,21 +585,23 @@ __global__ void __launch_bounds__(kLaunch, 1)
             ok = ok && tc::mbar_wait_hint(bar_pv + mb, (n - 1) & 1, p.err, kHintNs);
             tc::tc_fence_after();
           }
-          if (w == 0 && lane == 0) {               // this lane's row is the tile's first
-            tc::mbar_arrive_expect_tx(bar_full + mb, 2 * kKVBlk);
-            tc::tma_load_2d(sKV + 2 * mb * kKVBlk, &tm_rows, 128 * mb, code, bar_full + mb);
-            tc::tma_load_2d(sKV + (2 * mb + 1) * kKVBlk, &tm_rows, 128 * mb + 64, code, bar_full + mb);
+          if (mb == 0) {
+            if (lane == 0) s_valid16[w] = (uint16_t)have;
+            if (wait_q) tc::cp_async_wait_all();
+          }
+          if (w == 0) {                            // lane 0's row is the tile's first
+            tc::fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              tc::mbar_arrive_expect_tx(bar_full + mb, 2 * kKVBlk);
+              tc::tma_load_2d(sKV + 2 * mb * kKVBlk, &tm_rows, 128 * mb, code, bar_full + mb);
+              tc::tma_load_2d(sKV + (2 * mb + 1) * kKVBlk, &tm_rows, 128 * mb + 64, code, bar_full + mb);
+            }
+          } else {
+            warp_arrive(bar_full + mb, lane);
           }
         }
         row_page(nx, S.it.seq, p);
-        if (lane == 0) s_valid16[w] = (uint16_t)have;
-        if (wait_q) tc::cp_async_wait_all();
-#pragma unroll
-        for (int mb = 0; mb < 4; ++mb) {
-          ok = ok && tc::mbar_wait_hint(bar_full + mb, n_tma & 1, p.err, kHintNs);
-          pair_landed(mb);
-        }
-        ++n_tma;
       } else if (FP8 && !window) {
         // one copy of the code for pairs 0-2 (the staged registers move up a pair each time):
         // unrolled, the producers' instructions did not stay in the instruction cache
@@ -609,7 +631,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
             if (lane == 0) s_valid16[w] = (uint16_t)have;
             if (wait_q) tc::cp_async_wait_all();
           }
-          pair_landed(mb);
+          warp_arrive(bar_full + mb, lane);
 #pragma unroll
           for (int i = 0; i < 8; ++i) st[i] = st[i + 4];
           if (mb == 1) load_fp8_last(st, c4, p, lane);
@@ -627,7 +649,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
             if (lane == 0) s_valid16[w] = (uint16_t)have;
             if (wait_q) tc::cp_async_wait_all();
           }
-          pair_landed(mb);
+          warp_arrive(bar_full + mb, lane);
           if (mb < 2) load_bf16(st, mb + 2, p, window, c4, lane);
           if (mb == 2) row_page(nx, S.it.seq, p);
         }
