@@ -64,11 +64,11 @@ constexpr int kBarS = kST + 32;       // threads of a barrier of the softmax and
 constexpr int kBarW = 64;             // ... of the watching and the MMA warp
 constexpr int kLaunch = 640;
 // Registers a thread by warpgroup (2 x softmax, 2 x producers, MMA), out of 5 x 96 at launch.
-constexpr int kRegsSoftmax = 96, kRegsProd = 128, kRegsMma = 32;
+constexpr int kRegsSoftmax = 80, kRegsProd = 144, kRegsMma = 32;
 constexpr int kRegsLaunch = 96;       // 65,536 / 640, whole multiples of 8
 // .dec must not raise a warpgroup's count and .inc must not lower it (either faults), and the
 // shares must fit what the block was launched with (or .inc waits for good).
-static_assert(kRegsSoftmax >= kRegsLaunch && kRegsProd >= kRegsLaunch && kRegsMma <= kRegsLaunch &&
+static_assert(kRegsSoftmax <= kRegsLaunch && kRegsProd >= kRegsLaunch && kRegsMma <= kRegsLaunch &&
                   2 * kRegsSoftmax + 2 * kRegsProd + kRegsMma <= 5 * kRegsLaunch, "setmaxnreg shares");
 constexpr uint32_t kHintNs = 64;
 constexpr int kSeqCache = 1024;       // sequences whose boundaries are kept in shared memory
@@ -194,7 +194,7 @@ __device__ __forceinline__ uint8_t* tile_at(uint8_t* sKV, int row, int cb, int c
   return sKV + cb * kKVBlk + row * 128 + ((cc ^ (row & 7)) << 4);
 }
 
-constexpr int kStage = 16;   // 16-byte registers a producer thread stages of the next tile
+constexpr int kStage = 18;   // 16-byte registers a producer thread stages of the next tile
 
 // A producer warp moves 16 rows of the tile; lane = (row of four, 16-byte chunk of eight): rows
 // 4 i + lane / 8, i < 4, 128 contiguous bytes of a row at a time (64-byte pieces
@@ -235,40 +235,33 @@ __device__ __forceinline__ void store_bf16(const uint4 (&st)[kStage], int mb, ui
       sts16(tile_at(sKV, row0 + 4 * i + (lane >> 3), 2 * mb + j, lane & 7), st[8 * (mb & 1) + 2 * i + j]);
   }
 }
-// FP8 rows: pairs 0-2 are staged (a row's 128 codes of a pair are eight lanes' chunks); pair 3
-// (the last 64 codes and the 64 bf16 dims) is loaded into the registers of pairs 0 and 1 as
-// those are stored.  The scale words of the quarter's rows stay with their rows' lanes.
+// FP8 rows: the whole tile is staged.  Pairs 0-2, a row's 128 codes of a pair being eight lanes'
+// chunks: st[4 mb ..+3]; pair 3: the last 64 codes, lane = (row of eight, chunk of four):
+// st[12..13], and the 64 bf16 dims: st[14..17].  The scale words of the warp's rows stay with
+// their rows' lanes.
 __device__ __forceinline__ void load_fp8(uint4 (&st)[kStage], uint2& sc, const int (&c)[4], const ChunkTc& p,
                                          int code, int lane) {
+  const uint8_t* rows = static_cast<const uint8_t*>(p.kv.rows);
+  const __nv_bfloat16* hi = static_cast<const __nv_bfloat16*>(p.kv.hi);
+  int cl[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) cl[i] = __shfl_sync(0xffffffffu, code, 8 * i + (lane >> 2));
   sc = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);       // a row that does not exist: zeros times 1
   if (code >= 0)
     sc = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.kv.scales) + (long long)code * 8));
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint8_t* a = (c[i] >= 0 ? static_cast<const uint8_t*>(p.kv.rows) + (long long)c[i] * kNc : g_zero_row) +
-                       16 * (lane & 7);
+    const uint8_t* a = (c[i] >= 0 ? rows + (long long)c[i] * kNc : g_zero_row) + 16 * (lane & 7);
 #pragma unroll
     for (int mb = 0; mb < 3; ++mb) st[4 * mb + i] = ldg_stream(a + 128 * mb);
   }
-}
-// Pair 3 into st[4..9]: two chunks of codes, lane = (row of eight, chunk of four), then the four
-// rows' bf16 dims.
-__device__ __forceinline__ void load_fp8_last(uint4 (&st)[kStage], const int (&c)[4], const ChunkTc& p,
-                                              int lane) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    st[12 + i] = ldg_stream((cl[i] >= 0 ? rows + (long long)cl[i] * kNc + 384 : g_zero_row) + 16 * (lane & 3));
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint8_t* h = c[i] >= 0 ? reinterpret_cast<const uint8_t*>(static_cast<const __nv_bfloat16*>(p.kv.hi) +
-                                                                    (long long)c[i] * kHi)
-                                 : g_zero_row;
-    st[6 + i] = ldg_stream(h + 16 * (lane & 7));
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int x = __shfl_sync(0xffffffffu, c[2 * i], ((lane >> 2) & 3) * 8);
-    const int y = __shfl_sync(0xffffffffu, c[2 * i + 1], ((lane >> 2) & 3) * 8);
-    const int r = lane & 16 ? y : x;
-    st[4 + i] = ldg_stream((r >= 0 ? static_cast<const uint8_t*>(p.kv.rows) + (long long)r * kNc + 384 : g_zero_row) +
-                           16 * (lane & 3));
+    const uint8_t* h = c[i] >= 0 ? reinterpret_cast<const uint8_t*>(hi + (long long)c[i] * kHi) : g_zero_row;
+    st[14 + i] = ldg_stream(h + 16 * (lane & 7));
   }
 }
 // Four codes times 2^k as four bf16 values, exactly.  Fast: two codes to f16 in one conversion,
@@ -304,40 +297,38 @@ __device__ __forceinline__ bool scales_fast(const uint2& sc) {
   for (int g = 0; g < 7; ++g) ok &= (((g < 4 ? sc.x : sc.y) >> (8 * (g & 3))) & 0xffu) - 113u <= 142u - 113u;
   return ok;
 }
-// Two of the lane's chunks of a pair, st[2 half ..+1] (kLast: pair 3's codes, half 0 alone), as
-// bf16, and their store.  Lanes 4-7 of eight store their two 16-byte pieces in the other order,
-// so that eight lanes hit 128 distinct bytes.
-template <bool kLast>
-__device__ __forceinline__ void convert_fp8(const uint4 (&st)[kStage], const uint2& sc, int mb, int half,
-                                            uint4 (&cv)[4], int lane) {
+// The lane's chunks of pair mb as bf16, and their store.  Lanes 4-7 of eight store their two
+// 16-byte pieces in the other order, so that eight lanes hit 128 distinct bytes.
+template <int mb>
+__device__ __forceinline__ void convert_fp8(const uint4 (&st)[kStage], const uint2& sc, uint4 (&cv)[8], int lane) {
   const uint32_t word = mb < 2 ? sc.x : sc.y;      // groups 4 (mb / 2) ..+3
-  const int shift = kLast ? 16 : 16 * (mb & 1) + 8 * ((lane >> 2) & 1);
+  const int shift = mb == 3 ? 16 : 16 * (mb & 1) + 8 * ((lane >> 2) & 1);
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const uint4 v = st[2 * half + x];
-    const int row = kLast ? 8 * x + (lane >> 2) : 4 * (2 * half + x) + (lane >> 3);
+  for (int x = 0; x < (mb == 3 ? 2 : 4); ++x) {
+    const uint4 v = st[4 * mb + x];
+    const int row = mb == 3 ? 8 * x + (lane >> 2) : 4 * x + (lane >> 3);
     const uint32_t s = (((__shfl_sync(0xffffffffu, word, row) >> shift) & 0xffu) - 112u) * 0x04000400u;
     const uint2 a = codes_fast(v.x, s), b = codes_fast(v.y, s), c = codes_fast(v.z, s), d = codes_fast(v.w, s);
     cv[2 * x] = make_uint4(a.x, a.y, b.x, b.y);
     cv[2 * x + 1] = make_uint4(c.x, c.y, d.x, d.y);
   }
 }
-template <bool kLast>
-__device__ __forceinline__ void store_fp8(const uint4 (&cv)[4], int mb, int half, uint8_t* sKV, int row0,
+template <int mb>
+__device__ __forceinline__ void store_fp8(const uint4 (&st)[kStage], const uint4 (&cv)[8], uint8_t* sKV, int row0,
                                           int lane) {
-  const int sw = kLast ? 0 : (lane >> 2) & 1;
+  const int sw = mb == 3 ? 0 : (lane >> 2) & 1;
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int r = row0 + (kLast ? 8 * x + (lane >> 2) : 4 * (2 * half + x) + (lane >> 3));
+  for (int x = 0; x < (mb == 3 ? 2 : 4); ++x) {
+    const int r = row0 + (mb == 3 ? 8 * x + (lane >> 2) : 4 * x + (lane >> 3));
     const int cb = 2 * mb + sw, cc = 2 * (lane & 3);
     const uint4 u = cv[2 * x], v = cv[2 * x + 1];
     sts16(tile_at(sKV, r, cb, cc + sw), sw ? v : u);
     sts16(tile_at(sKV, r, cb, cc + (sw ^ 1)), sw ? u : v);
   }
-}
-__device__ __forceinline__ void store_hi(const uint4 (&st)[kStage], uint8_t* sKV, int row0, int lane) {
+  if (mb == 3) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) sts16(tile_at(sKV, row0 + 4 * i + (lane >> 3), 7, lane & 7), st[2 + i]);
+    for (int i = 0; i < 4; ++i) sts16(tile_at(sKV, row0 + 4 * i + (lane >> 3), 7, lane & 7), st[14 + i]);
+  }
 }
 // A warp's part of a pair straight from memory, for a tile with a scale that codes_fast does
 // not take: lane = (row of 16, half of the pair's dims), one 16-byte piece after another.
@@ -603,39 +594,45 @@ __global__ void __launch_bounds__(kLaunch, 1)
         }
         row_page(nx, S.it.seq, p);
       } else if (FP8 && !window) {
-        // one copy of the code for pairs 0-2 (the staged registers move up a pair each time):
-        // unrolled, the producers' instructions did not stay in the instruction cache
-        const bool fast = __all_sync(0xffffffffu, scales_fast(sc));
-#pragma unroll 1
-        for (int mb = 0; mb < 4; ++mb) {
-          uint4 cv[4];
-          if (fast) {
-            if (mb < 3) convert_fp8<false>(st, sc, mb, 0, cv, lane);
-            else convert_fp8<true>(st, sc, mb, 0, cv, lane);
-          }
+        // pair 0 is converted while its place is still taken.  The PVs of the tile before end in
+        // order and faster than pairs are stored, so after the first the last is waited for.
+        auto wait_pv = [&](int mb) {
           if (n > 0) {
             ok = ok && tc::mbar_wait_hint(bar_pv + mb, (n - 1) & 1, p.err, kHintNs);
             tc::tc_fence_after();
           }
-          if (!fast) {
+        };
+        auto ready = [&]() {
+          if (lane == 0) s_valid16[w] = (uint16_t)have;
+          if (wait_q) tc::cp_async_wait_all();
+        };
+        if (__all_sync(0xffffffffu, scales_fast(sc))) {
+          uint4 cv[8];
+          convert_fp8<0>(st, sc, cv, lane);
+          wait_pv(0);
+          store_fp8<0>(st, cv, sKV, row0, lane);
+          ready();
+          warp_arrive(bar_full, lane);
+          convert_fp8<1>(st, sc, cv, lane);
+          wait_pv(3);
+          store_fp8<1>(st, cv, sKV, row0, lane);
+          warp_arrive(bar_full + 1, lane);
+          row_page(nx, S.it.seq, p);
+          convert_fp8<2>(st, sc, cv, lane);
+          store_fp8<2>(st, cv, sKV, row0, lane);
+          warp_arrive(bar_full + 2, lane);
+          convert_fp8<3>(st, sc, cv, lane);
+          store_fp8<3>(st, cv, sKV, row0, lane);
+          warp_arrive(bar_full + 3, lane);
+        } else {
+          wait_pv(3);
+          ready();
+          row_page(nx, S.it.seq, p);
+#pragma unroll 1
+          for (int mb = 0; mb < 4; ++mb) {
             move_fp8_slow(p, code, mb, sKV, myrow, lane >> 4);
-          } else if (mb < 3) {
-            store_fp8<false>(cv, mb, 0, sKV, row0, lane);
-            convert_fp8<false>(st, sc, mb, 1, cv, lane);
-            store_fp8<false>(cv, mb, 1, sKV, row0, lane);
-          } else {
-            store_fp8<true>(cv, mb, 0, sKV, row0, lane);
-            store_hi(st, sKV, row0, lane);
+            warp_arrive(bar_full + mb, lane);
           }
-          if (mb == 0) {
-            if (lane == 0) s_valid16[w] = (uint16_t)have;
-            if (wait_q) tc::cp_async_wait_all();
-          }
-          warp_arrive(bar_full + mb, lane);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) st[i] = st[i + 4];
-          if (mb == 1) load_fp8_last(st, c4, p, lane);
-          if (mb == 2) row_page(nx, S.it.seq, p);
         }
       } else {
 #pragma unroll
@@ -663,7 +660,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // ------------------------------------------------------------------ softmax and output
     const int qd = warp & 3, hf = warp >> 2;
     const uint32_t lane_addr = (uint32_t)(qd * 32) << 16;
