@@ -194,7 +194,10 @@ __device__ __forceinline__ uint8_t* tile_at(uint8_t* sKV, int row, int cb, int c
   return sKV + cb * kKVBlk + row * 128 + ((cc ^ (row & 7)) << 4);
 }
 
-constexpr int kStage = 18;   // 16-byte registers a producer thread stages of the next tile
+// 16-byte registers a producer thread stages of the next tile, and how many of a plain tile's
+// four 128-dim pairs they hold (more in the FP8 kernel, for its window tiles, spilled).
+template <bool FP8> constexpr int kStage = FP8 ? 18 : 24;
+template <bool FP8> constexpr int kPairs = FP8 ? 2 : 3;
 
 // A producer warp moves 16 rows of the tile; lane = (row of four, 16-byte chunk of eight): rows
 // 4 i + lane / 8, i < 4, 128 contiguous bytes of a row at a time (64-byte pieces
@@ -202,8 +205,8 @@ constexpr int kStage = 18;   // 16-byte registers a producer thread stages of th
 // places are shuffled to their lanes ahead of all loads: a shuffle between loads waits behind
 // them in the same queue.
 //
-// bf16 rows: two of a tile's four 128-dim pairs are staged; the other two are loaded into
-// their registers as those are stored.
+// bf16 rows: kPairs of a tile's four pairs are staged; the others are loaded into their
+// registers as those are stored.
 // Numbers of the four rows this lane loads.
 __device__ __forceinline__ void row_numbers(int (&c)[4], int code, int lane) {
 #pragma unroll
@@ -216,30 +219,32 @@ __device__ __forceinline__ const char* row_addr(const ChunkTc& p, bool window, i
   const char* a = reinterpret_cast<const char*>(base + (long long)(window ? code & (kNewTag - 1) : code) * kD);
   return code < 0 ? reinterpret_cast<const char*>(g_zero_row) : a;
 }
-__device__ __forceinline__ void load_bf16(uint4 (&st)[kStage], int mb, const ChunkTc& p, bool window,
+template <int NP, int N>
+__device__ __forceinline__ void load_bf16(uint4 (&st)[N], int mb, const ChunkTc& p, bool window,
                                           const int (&c)[4], int lane) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const char* a = row_addr(p, window, c[i]) + 16 * (lane & 7) + 256 * mb;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) st[8 * (mb & 1) + 2 * i + j] = ldg_stream(a + 128 * j);
+    for (int j = 0; j < 2; ++j) st[8 * (mb % NP) + 2 * i + j] = ldg_stream(a + 128 * j);
   }
 }
 __device__ __forceinline__ void sts16(uint8_t* d, const uint4& v) { sts16(d, v.x, v.y, v.z, v.w); }
-__device__ __forceinline__ void store_bf16(const uint4 (&st)[kStage], int mb, uint8_t* sKV, int row0,
+template <int NP, int N>
+__device__ __forceinline__ void store_bf16(const uint4 (&st)[N], int mb, uint8_t* sKV, int row0,
                                            int lane) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      sts16(tile_at(sKV, row0 + 4 * i + (lane >> 3), 2 * mb + j, lane & 7), st[8 * (mb & 1) + 2 * i + j]);
+      sts16(tile_at(sKV, row0 + 4 * i + (lane >> 3), 2 * mb + j, lane & 7), st[8 * (mb % NP) + 2 * i + j]);
   }
 }
 // FP8 rows: the whole tile is staged.  Pairs 0-2, a row's 128 codes of a pair being eight lanes'
 // chunks: st[4 mb ..+3]; pair 3: the last 64 codes, lane = (row of eight, chunk of four):
 // st[12..13], and the 64 bf16 dims: st[14..17].  The scale words of the warp's rows stay with
 // their rows' lanes.
-__device__ __forceinline__ void load_fp8(uint4 (&st)[kStage], uint2& sc, const int (&c)[4], const ChunkTc& p,
+__device__ __forceinline__ void load_fp8(uint4 (&st)[kStage<true>], uint2& sc, const int (&c)[4], const ChunkTc& p,
                                          int code, int lane) {
   const uint8_t* rows = static_cast<const uint8_t*>(p.kv.rows);
   const __nv_bfloat16* hi = static_cast<const __nv_bfloat16*>(p.kv.hi);
@@ -300,7 +305,7 @@ __device__ __forceinline__ bool scales_fast(const uint2& sc) {
 // The lane's chunks of pair mb as bf16, and their store.  Lanes 4-7 of eight store their two
 // 16-byte pieces in the other order, so that eight lanes hit 128 distinct bytes.
 template <int mb>
-__device__ __forceinline__ void convert_fp8(const uint4 (&st)[kStage], const uint2& sc, uint4 (&cv)[8], int lane) {
+__device__ __forceinline__ void convert_fp8(const uint4 (&st)[kStage<true>], const uint2& sc, uint4 (&cv)[8], int lane) {
   const uint32_t word = mb < 2 ? sc.x : sc.y;      // groups 4 (mb / 2) ..+3
   const int shift = mb == 3 ? 16 : 16 * (mb & 1) + 8 * ((lane >> 2) & 1);
 #pragma unroll
@@ -314,7 +319,7 @@ __device__ __forceinline__ void convert_fp8(const uint4 (&st)[kStage], const uin
   }
 }
 template <int mb>
-__device__ __forceinline__ void store_fp8(const uint4 (&st)[kStage], const uint4 (&cv)[8], uint8_t* sKV, int row0,
+__device__ __forceinline__ void store_fp8(const uint4 (&st)[kStage<true>], const uint4 (&cv)[8], uint8_t* sKV, int row0,
                                           int lane) {
   const int sw = mb == 3 ? 0 : (lane >> 2) & 1;
 #pragma unroll
@@ -514,7 +519,8 @@ __global__ void __launch_bounds__(kLaunch, 1)
     const int row0 = 16 * w;                       // this warp's rows of a tile
     const int myrow = row0 + (lane & 15);          // the one whose place this lane finds out
     bool ok = true;
-    uint4 st[kStage];
+    constexpr int NP = kPairs<FP8>;
+    uint4 st[kStage<FP8>];
     uint2 sc = make_uint2(0u, 0u);                 // FP8: the scales of this lane's row, and the
     int c4[4];                                     // numbers of the four rows it loads
     Stream S;
@@ -547,10 +553,10 @@ __global__ void __launch_bounds__(kLaunch, 1)
       whole = !FP8 && !window && !p.idx && (S.tile + 1) * kRows <= S.it.nsel && have == 0xffffffffu;
       row_numbers(c4, code, lane);
       if (FP8 && !window) {
-        load_fp8(st, sc, c4, p, code, lane);
+        if constexpr (FP8) load_fp8(st, sc, c4, p, code, lane);
       } else if (!whole) {
-        load_bf16(st, 0, p, window, c4, lane);
-        load_bf16(st, 1, p, window, c4, lane);
+#pragma unroll
+        for (int mb = 0; mb < NP; ++mb) load_bf16<NP>(st, mb, p, window, c4, lane);
       }
       if (!new_q) {
         ++S.tile;
@@ -569,17 +575,23 @@ __global__ void __launch_bounds__(kLaunch, 1)
     queries();
     for (uint32_t n = 0; live; ++n) {
       const bool wait_q = new_q;
+      // (the PVs of the tile before end in order, and faster than pairs are stored: a staged tile
+      // waits for the first and then for the last)
+      auto wait_pv = [&](int mb) {
+        if (n > 0) {
+          ok = ok && tc::mbar_wait_hint(bar_pv + mb, (n - 1) & 1, p.err, kHintNs);
+          tc::tc_fence_after();
+        }
+      };
+      auto ready = [&]() {
+        if (lane == 0) s_valid16[w] = (uint16_t)have;
+        if (wait_q) tc::cp_async_wait_all();
+      };
       if (!FP8 && whole) {
 #pragma unroll
         for (int mb = 0; mb < 4; ++mb) {
-          if (n > 0) {
-            ok = ok && tc::mbar_wait_hint(bar_pv + mb, (n - 1) & 1, p.err, kHintNs);
-            tc::tc_fence_after();
-          }
-          if (mb == 0) {
-            if (lane == 0) s_valid16[w] = (uint16_t)have;
-            if (wait_q) tc::cp_async_wait_all();
-          }
+          wait_pv(mb);
+          if (mb == 0) ready();
           if (w == 0) {                            // lane 0's row is the tile's first
             tc::fence_proxy_async();
             __syncwarp();
@@ -594,21 +606,10 @@ __global__ void __launch_bounds__(kLaunch, 1)
         }
         row_page(nx, S.it.seq, p);
       } else if (FP8 && !window) {
-        // pair 0 is converted while its place is still taken.  The PVs of the tile before end in
-        // order and faster than pairs are stored, so after the first the last is waited for.
-        auto wait_pv = [&](int mb) {
-          if (n > 0) {
-            ok = ok && tc::mbar_wait_hint(bar_pv + mb, (n - 1) & 1, p.err, kHintNs);
-            tc::tc_fence_after();
-          }
-        };
-        auto ready = [&]() {
-          if (lane == 0) s_valid16[w] = (uint16_t)have;
-          if (wait_q) tc::cp_async_wait_all();
-        };
+        if constexpr (FP8) {
         if (__all_sync(0xffffffffu, scales_fast(sc))) {
           uint4 cv[8];
-          convert_fp8<0>(st, sc, cv, lane);
+          convert_fp8<0>(st, sc, cv, lane);         // while its place is still taken
           wait_pv(0);
           store_fp8<0>(st, cv, sKV, row0, lane);
           ready();
@@ -634,20 +635,15 @@ __global__ void __launch_bounds__(kLaunch, 1)
             warp_arrive(bar_full + mb, lane);
           }
         }
+        }
       } else {
 #pragma unroll
         for (int mb = 0; mb < 4; ++mb) {
-          if (n > 0) {
-            ok = ok && tc::mbar_wait_hint(bar_pv + mb, (n - 1) & 1, p.err, kHintNs);
-            tc::tc_fence_after();
-          }
-          store_bf16(st, mb, sKV, row0, lane);
-          if (mb == 0) {
-            if (lane == 0) s_valid16[w] = (uint16_t)have;
-            if (wait_q) tc::cp_async_wait_all();
-          }
+          if (mb < 2) wait_pv(mb == 0 ? 0 : 3);
+          store_bf16<NP>(st, mb, sKV, row0, lane);
+          if (mb == 0) ready();
           warp_arrive(bar_full + mb, lane);
-          if (mb < 2) load_bf16(st, mb + 2, p, window, c4, lane);
+          if (mb + NP < 4) load_bf16<NP>(st, mb + NP, p, window, c4, lane);
           if (mb == 2) row_page(nx, S.it.seq, p);
         }
       }
