@@ -81,7 +81,7 @@ struct ChunkTc {
   const float* sink;
   __nv_bfloat16* out;
   float* lse;
-  float *part_o, *part_m, *part_l;   // per item [512][64], [64], [64]
+  float *part_o, *part_m, *part_l;   // per item [64][512], [64], [64]
   int* err;
   csa_kv_cache kv;
   int b, N, n_w, m, k, nsplit, items, d_rope_out;
@@ -840,22 +840,17 @@ __global__ void __launch_bounds__(kLaunch, 1)
       }
       tc::named_bar(3, kST);
       if (p.nsplit > 1) {
+        // lanes are neighbouring dims: a head's 32 dims leave as one 128-byte line
 #pragma unroll 1
-        for (int mb = 2 * hf; mb < 2 * hf + 2; ++mb) {
+        for (int mb = 0; mb < 4; ++mb) {
           ok = ok && tc::mbar_wait_hint(bar_pv + mb, (ns - 1) & 1, p.err, kHintNs);
           tc::tc_fence_after();
+          uint32_t o[32];
+          tc::tmem_ld32(tO + mb * kH + 32 * hf + lane_addr, o);
+          tc::tmem_ld_wait(o);
+          float* dst = p.part_o + ((long long)item * kH + 32 * hf) * kD + mb * 128 + row;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t o[32];
-            tc::tmem_ld32(tO + mb * kH + half * 32 + lane_addr, o);
-            tc::tmem_ld_wait(o);
-            float4* dst = reinterpret_cast<float4*>(p.part_o + ((long long)item * kD + mb * 128 + row) * kH + half * 32);
-#pragma unroll
-            for (int h4 = 0; h4 < 8; ++h4)
-              dst[h4] = ok ? make_float4(__uint_as_float(o[4 * h4]), __uint_as_float(o[4 * h4 + 1]),
-                                         __uint_as_float(o[4 * h4 + 2]), __uint_as_float(o[4 * h4 + 3]))
-                           : make_float4(nan_f(), nan_f(), nan_f(), nan_f());
-          }
+          for (int h = 0; h < 32; ++h) dst[h * kD] = ok ? __uint_as_float(o[h]) : nan_f();
         }
       } else {
 #pragma unroll 1
@@ -903,42 +898,38 @@ __global__ void __launch_bounds__(kLaunch, 1)
   }
 }
 
-// Combines the splits of a token: CTA per (token, 16 dims), thread per (head, 4 dims).  The
-// weights e^(m_s - top) / den of every split come first, then each thread adds its four dims
-// over the splits (coalesced over the heads).
-constexpr int kMergeDims = 16;
-__global__ void __launch_bounds__(256) chunk_merge_kernel(ChunkTc p) {
-  __shared__ float s_w[kMaxSplit][kH];
-  const int tok = blockIdx.x, tid = threadIdx.x;
-  const int h = tid & (kH - 1), d = blockIdx.y * kMergeDims + 4 * (tid >> 6);
-  const int seq = find_seq(p.cu_q, p.b, tok, tid & 31);
+// Combines the splits of a token: CTA per (token, two heads), four warps a head, four dims a
+// thread.  A lane holds one split's weight e^(m_s - top) / den, found by the warp's reductions
+// over the splits; the partial rows are added in batches of loads, those of empty splits (not
+// written, weight 0) dropped after the load, so that no load waits for another (a branch around
+// each took 7.7 us for 8 tokens of 17 splits).
+constexpr int kMergeHeads = 2;
+__global__ void __launch_bounds__(128 * kMergeHeads) chunk_merge_kernel(const __grid_constant__ ChunkTc p) {
+  const int tok = blockIdx.x, lane = threadIdx.x & 31;
+  const int h = blockIdx.y * kMergeHeads + (threadIdx.x >> 7), d = 4 * (threadIdx.x & 127);
+  const int seq = find_seq(p.cu_q, p.b, tok, lane);
   if (seq >= p.b || tok < p.cu_q[0]) return;
   const int t = p.pos0[seq] + (tok - p.cu_q[seq]);
   const float sink2 = p.sink[h] * kLog2e;
   pdl_wait();
   const long long it0 = (long long)tok * p.nsplit;
-  if (tid < kH) {
-    float top = sink2;
-    for (int s = 0; s < p.nsplit; ++s) top = fmaxf(top, p.part_m[(it0 + s) * kH + h]);
-    float den = rel_weight(sink2, top);
-    for (int s = 0; s < p.nsplit; ++s) {
-      const float w = rel_weight(p.part_m[(it0 + s) * kH + h], top);
-      s_w[s][h] = w;
-      den = fmaf(p.part_l[(it0 + s) * kH + h], w, den);
-    }
-    const float inv = den == 0.f ? 0.f : 1.f / den;
-    for (int s = 0; s < p.nsplit; ++s) s_w[s][h] *= inv;
-    if (p.lse && blockIdx.y == 0)
-      p.lse[(long long)tok * kH + h] = den == 0.f ? -INFINITY : (top + log2f(den)) * kLn2;
-  }
-  __syncthreads();
+  const float m = lane < p.nsplit ? p.part_m[(it0 + lane) * kH + h] : -INFINITY;
+  const float l = lane < p.nsplit ? p.part_l[(it0 + lane) * kH + h] : 0.f;
+  const float top = fmaxf(warp_max(m), sink2);
+  float w = rel_weight(m, top);
+  const float den = warp_sum(l * w) + rel_weight(sink2, top);
+  w = den == 0.f ? 0.f : w / den;
+  if (p.lse && d == 0) p.lse[(long long)tok * kH + h] = den == 0.f ? -INFINITY : (top + log2f(den)) * kLn2;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  const float* src = p.part_o + (it0 * kH + h) * kD + d;
+#pragma unroll 8
   for (int s = 0; s < p.nsplit; ++s) {
-    const float w = s_w[s][h];
-    if (w == 0.f) continue;                        // an empty split's O is not written
-    const float* src = p.part_o + ((it0 + s) * kD + d) * kH + h;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) acc[u] = fmaf(src[u * kH], w, acc[u]);
+    const float4 v = *reinterpret_cast<const float4*>(src + (long long)s * kH * kD);
+    const float ws = __shfl_sync(0xffffffffu, w, s);
+    acc[0] = ws == 0.f ? acc[0] : fmaf(v.x, ws, acc[0]);
+    acc[1] = ws == 0.f ? acc[1] : fmaf(v.y, ws, acc[1]);
+    acc[2] = ws == 0.f ? acc[2] : fmaf(v.z, ws, acc[2]);
+    acc[3] = ws == 0.f ? acc[3] : fmaf(v.w, ws, acc[3]);
   }
 #pragma unroll
   for (int u = 0; u < 4; u += 2) {
@@ -968,18 +959,21 @@ int sm_count() {
   return sms;
 }
 
-// Splits per token.  A CTA's time for an item of n tiles is about n + 1.5 tiles (queries,
-// the first tile's latency, the output); the CTAs work through ceil(N splits / SMs) items
-// each; a merge costs about three tiles.
+// Splits per token.  In units of a tile's time: a CTA's item of n tiles costs about n + 1.5 (its
+// queries, the first tile's latency, the output), the CTAs work through ceil(N splits / SMs)
+// items each, and the partials of an item about 0.015 in all.  With two tokens per SM or more
+// splitting only multiplies the items' overhead (and their tokens may be far shorter than
+// L_max says): never.
 int plan_splits(int n_w, int m, int k, int N, int L_max) {
   const int E = k > 0 ? k : L_max / m;
   const int tiles = (E + kRows - 1) / kRows + (n_w + kRows - 1) / kRows;
   const int sms = sm_count();
   int best = 1;
   double least = 0;
+  if (N >= 2 * sms) return best;
   for (int ns = 1; ns <= std::min(kMaxSplit, std::max(tiles, 1)); ++ns) {
     const double rounds = (double)(((long long)N * ns + sms - 1) / sms);
-    const double cost = rounds * ((tiles + ns - 1) / ns + 1.5) + (ns > 1 ? 3.0 : 0.0);
+    const double cost = rounds * ((tiles + ns - 1) / ns + 1.5) + (ns > 1 ? 1.0 + 0.015 * N * ns : 0.0);
     if (ns == 1 || cost < least) { best = ns; least = cost; }
   }
   return best;
@@ -1040,7 +1034,7 @@ csa_status launch_chunk_attn_tc(const ChunkArgs& a, const csa_kv_cache& kv, void
   const int grid = (int)std::min<long long>(items, sm_count());
   if (csa_launch(kern, dim3(grid), dim3(kLaunch), kSmem, st, false, tm, p) != cudaSuccess) return CSA_ERR_CUDA;
   if (p.nsplit > 1 &&
-      csa_launch(chunk_merge_kernel, dim3(a.N, kD / kMergeDims), dim3(256), 0, st, true, p) != cudaSuccess)
+      csa_launch(chunk_merge_kernel, dim3(a.N, kH / kMergeHeads), dim3(128 * kMergeHeads), 0, st, true, p) != cudaSuccess)
     return CSA_ERR_CUDA;
   return CSA_OK;
 }
