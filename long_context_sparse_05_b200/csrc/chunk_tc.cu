@@ -380,6 +380,21 @@ __device__ __forceinline__ void tmem_ld16(uint32_t ta, uint32_t (&r)[16]) {
       :: "memory");
 }
 
+// 32 TMEM lanes x 16 columns: lane l gets its lane's columns.
+__device__ __forceinline__ void tmem_ld_x16(uint32_t ta, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(ta) : "memory");
+  asm volatile(
+      "tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+      :: "memory");
+}
+
 // The query heads of a token into shared memory (cp.async, by the producer warps).
 __device__ __forceinline__ void load_q(const ChunkTc& p, int tok, uint8_t* sQ, int warp, int lane) {
   const __nv_bfloat16* qb = p.q + (long long)tok * kH * kD;
@@ -853,35 +868,43 @@ __global__ void __launch_bounds__(kLaunch, 1)
           for (int h = 0; h < 32; ++h) dst[h * kD] = ok ? __uint_as_float(o[h]) : nan_f();
         }
       } else {
+        // 16 heads at a time, their factors in registers over the four dim blocks (a shared-memory
+        // read for each pair of heads and block cost 7 % of a selected chunk)
+        const int odd = lane & 1, d0 = row & ~1;
 #pragma unroll 1
-        for (int mb = 0; mb < 4; ++mb) {
-          ok = ok && tc::mbar_wait_hint(bar_pv + mb, (ns - 1) & 1, p.err, kHintNs);
-          tc::tc_fence_after();
-          uint32_t o[32];
-          tc::tmem_ld32(tO + mb * kH + 32 * hf + lane_addr, o);
-          tc::tmem_ld_wait(o);
-          // lanes 2i and 2i + 1 hold dims 2i and 2i + 1 of every head: the even lane takes both
-          // of head h, the odd one both of head h + 1, for 4-byte stores and the rotary pair
-          const int d = mb * 128 + (row & ~1);
-          const bool rot = d >= kD - p.d_rope_out;
-          float sn = 0.f, cs = 1.f;
-          if (rot) rope_angle((double)I.t * p.inv_freq[(d - (kD - p.d_rope_out)) >> 1], &sn, &cs);
+        for (int hh = 0; hh < 32; hh += 16) {
+          float w[16];
 #pragma unroll
-          for (int h = 0; h < 32; h += 2) {
-            const float2 w = *reinterpret_cast<const float2*>(s_alpha + 32 * hf + h);
-            const float a = w.x == 0.f ? 0.f : __uint_as_float(o[h]) * w.x;
-            const float c = w.y == 0.f ? 0.f : __uint_as_float(o[h + 1]) * w.y;
-            const bool odd = lane & 1;
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? a : c, 1);
-            float x0 = odd ? got : a, x1 = odd ? c : got;
-            if (rot) {
-              const float y0 = fmaf(x0, cs, x1 * sn), y1 = fmaf(x1, cs, -x0 * sn);
-              x0 = y0; x1 = y1;
+          for (int h = 0; h < 16; h += 4) {
+            const float4 w4 = *reinterpret_cast<const float4*>(s_alpha + 32 * hf + hh + h);
+            w[h] = w4.x; w[h + 1] = w4.y; w[h + 2] = w4.z; w[h + 3] = w4.w;
+          }
+#pragma unroll 1
+          for (int mb = 0; mb < 4; ++mb) {
+            if (hh == 0) ok = ok && tc::mbar_wait_hint(bar_pv + mb, (ns - 1) & 1, p.err, kHintNs);
+            tc::tc_fence_after();
+            uint32_t o[16];
+            tmem_ld_x16(tO + mb * kH + 32 * hf + hh + lane_addr, o);
+            // lanes 2i and 2i + 1 hold dims 2i and 2i + 1 of every head: the even lane takes both
+            // of head h, the odd one both of head h + 1, for 4-byte stores and the rotary pair
+            const int d = mb * 128 + d0;
+            const bool rot = d >= kD - p.d_rope_out;
+            float sn = 0.f, cs = 1.f;
+            if (rot) rope_angle((double)I.t * p.inv_freq[(d - (kD - p.d_rope_out)) >> 1], &sn, &cs);
+            __nv_bfloat16* dst = p.out + ((long long)I.tok * kH + 32 * hf + hh + odd) * kD + d;
+#pragma unroll
+            for (int h = 0; h < 16; h += 2) {
+              const float a = w[h] == 0.f ? 0.f : __uint_as_float(o[h]) * w[h];
+              const float c = w[h + 1] == 0.f ? 0.f : __uint_as_float(o[h + 1]) * w[h + 1];
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? a : c, 1);
+              float x0 = odd ? got : a, x1 = odd ? c : got;
+              if (rot) {
+                const float y0 = fmaf(x0, cs, x1 * sn), y1 = fmaf(x1, cs, -x0 * sn);
+                x0 = y0; x1 = y1;
+              }
+              if (!ok) x0 = x1 = nan_f();
+              *reinterpret_cast<__nv_bfloat162*>(dst + h * kD) = __floats2bfloat162_rn(x0, x1);
             }
-            if (!ok) x0 = x1 = nan_f();
-            *reinterpret_cast<__nv_bfloat162*>(
-                p.out + ((long long)I.tok * kH + 32 * hf + h + (odd ? 1 : 0)) * kD + d) =
-                __floats2bfloat162_rn(x0, x1);
           }
         }
       }
