@@ -273,7 +273,8 @@ class Case:
     """A ragged chunk over a paged cache with everything random, and its oracle."""
 
     def __init__(self, lens, ctx, H, d, m, k, n_w, dtype, fmt, d_hi=0, d_rope_out=0, seed=0,
-                 sink=None, pad=2, counts=None, hole=False, qscale=1.0):
+                 sink=None, pad=2, counts=None, hole=False, qscale=1.0, rscale=1.0, zero_group=False,
+                 nan_rest=False, dup=False):
         self.__dict__.update(lens=lens, ctx=ctx, H=H, d=d, m=m, k=k, n_w=n_w, dtype=dtype, fmt=fmt,
                              d_hi=d_hi)
         b, n = len(lens), sum(lens)
@@ -284,16 +285,41 @@ class Case:
         if hole and self.bt.shape[1] > 1:
             self.bt[0, 0] = total + 3                # a page outside the pool
         self.kv = cache_of(fmt, d, d_hi, total, self.bt)
-        rows = randn(seed + 1, (total * PE, d))
+        rows = randn(seed + 1, (total * PE, d)) * rscale
+        if zero_group:
+            rows[::3, :64] = 0.0                     # groups of zeros: the lowest scale
         if fmt == L.CSA_FP8_E4M3:
             flat = L.alloc_kv_cache(fmt, d, d_hi, total, i32([list(range(total))]))
             flat.rows, flat.hi, flat.scales = self.kv.rows, self.kv.hi, self.kv.scales
             L.csa_cache_write(flat, L.CSA_F32, rows, i32([0, total * PE]), i32([0]), 1, total * PE)
         else:
             self.kv._tensors[0].copy_(rows)
+        if nan_rest:
+            # every row that no token may see: NaN
+            seen = torch.zeros(total * PE, dtype=torch.bool)
+            for s, e in enumerate(ents):
+                for x in range(e):
+                    if 0 <= self.bt[s, x // PE] < total:
+                        seen[place(self.bt, s, x)] = True
+            hid = (~seen).cuda()
+            if fmt == L.CSA_FP8_E4M3:
+                self.kv._tensors[0][hid] = 0x7F
+                self.kv._tensors[1][hid] = float("nan")
+                self.kv._tensors[2][hid] = 0xFF
+            else:
+                self.kv._tensors[0][hid] = float("nan")
         self.q = (randn(seed + 2, (self.N, H, d)) * qscale).to(dt)
         self.win = randn(seed + 3, (b, max(n_w, 1), d), dt)
         self.new_win = randn(seed + 4, (self.N, d), dt)
+        if rscale != 1.0:
+            self.win *= rscale
+            self.new_win *= rscale
+        if nan_rest:
+            for s in range(b):                       # ring slots before the sequence's first token
+                for u in range(ctx[s] - max(n_w, 1), min(0, ctx[s])):
+                    self.win[s, u % max(n_w, 1)] = float("nan")
+            self.new_win[self.cu[-1]:] = float("nan")
+            self.q[self.cu[-1]:] = float("nan")
         self.sink = randn(seed + 5, (H,)) if sink is None else torch.full((H,), sink, device="cuda")
         self.idx = self.count = None
         if k:
@@ -305,6 +331,9 @@ class Case:
                     r = self.cu[s] + i
                     c = min(E, k) if counts is None else min(counts, k)
                     pick = np.sort(rng.choice(E, min(E, c), replace=False)) if E else np.zeros(0, int)
+                    if dup and len(pick) > 2:
+                        pick[1] = pick[0]            # an entry named twice counts twice
+                        pick[-1] = 2 ** 31 - 1       # and one far outside the table
                     idx[r, :len(pick)] = pick
                     count[r] = c
             self.idx, self.count = i32(idx.tolist()), i32(count.tolist())
@@ -441,3 +470,259 @@ def test_chunk_attn_small_shape_edges():
         c = dict(SMALL, lens=[5, 3], ctx=[2500, 1], seed=41)
         c.update(cfg)
         Case(**c).run().check()
+
+
+@pytest.mark.parametrize("fmt,d_hi", [(L.CSA_BF16, 0), (L.CSA_FP8_E4M3, 64)])
+@pytest.mark.parametrize("cfg", [
+    dict(lens=[303], ctx=[2600], k=700, qscale=20.0),             # many tiles in one CTA, maxima that rise
+    dict(lens=[200, 130], ctx=[4000, 17], k=0),                   # whole tiles, partial ones, two windows
+    dict(lens=[303], ctx=[2600], k=0, qscale=20.0, n_w=5),
+    dict(lens=[303], ctx=[2400], k=650, hole=True),               # tiles without a row before the first with one
+    dict(lens=[303], ctx=[2400], k=0, hole=True, sink=-math.inf, n_w=0),
+    dict(lens=[150, 160], ctx=[3000, 900], k=300, nan_rest=True),
+    dict(lens=[150, 160], ctx=[3000, 60], k=0, nan_rest=True, n_w=130),
+    dict(lens=[40], ctx=[5000], k=0, nan_rest=True),              # the same with the rows split over CTAs
+    dict(lens=[301], ctx=[1500], k=300, rscale=2.0 ** 30, qscale=2.0 ** -30),   # scales beyond f16
+    dict(lens=[301], ctx=[1500], k=300, zero_group=True),
+    dict(lens=[9], ctx=[1500], k=300, zero_group=True, rscale=2.0 ** -20, qscale=2.0 ** 20),
+    dict(lens=[301, 20], ctx=[1500, 90], k=64, dup=True),
+    dict(lens=[7], ctx=[1500], k=200, dup=True),
+    dict(lens=[160, 140], ctx=[128 * 70, 128 * 3], k=0, m=128),
+])
+def test_chunk_attn_many_tiles(fmt, d_hi, cfg):
+    c = dict(TC, m=4, seed=51, fmt=fmt, d_hi=d_hi, d_rope_out=64)
+    c.update(cfg)
+    Case(**c).run().check(tokens=5)
+
+
+@pytest.mark.parametrize("fmt,d_hi,shape", [(L.CSA_BF16, 0, "tc"), (L.CSA_FP8_E4M3, 64, "tc"), (L.CSA_F32, 0, "small")])
+def test_chunk_attn_counts_out_of_range(fmt, d_hi, shape):
+    """A negative count selects nothing, one above k all k slots."""
+    cfg = dict(TC, m=4) if shape == "tc" else dict(SMALL)
+    cfg["fmt"] = fmt
+    c = Case([4], [900], k=32, d_hi=d_hi, seed=61, **cfg)
+    want = c.count.clone()
+    c.count[0], c.count[1] = -7, 32 + 1000
+    c.run()
+    c.count = want
+    c.count[0], c.count[1] = 0, 32
+    c.check()
+
+
+@pytest.mark.parametrize("b", [33, 1100])
+def test_chunk_attn_many_sequences(b):
+    """More sequences than one step of the search, and than shared memory holds."""
+    rng = np.random.default_rng(b)
+    lens = [int(x) for x in rng.integers(0, 3, b)]
+    ctx = [int(x) for x in rng.integers(0, 600, b)]
+    c = Case(lens, ctx, m=4, k=0, fmt=L.CSA_BF16, seed=71, **TC).run()
+    c.rows64 = c.values()
+    full = c.b
+    # a sample of the sequences
+    keep = [s for s in range(full) if lens[s]][:: max(1, full // 12)]
+    q, win, nw, sink = f64(c.q), f64(c.win), f64(c.new_win), f64(c.sink)
+    for s in keep:
+        for i in range(lens[s]):
+            _, rows = chunk.chunk_rows(s, i, c.entry, None, ctx[s], c.cu[s], 4, c.bt.shape[1] * PE, win, nw, 128)
+            o, l, A = chunk.attend(q[c.cu[s] + i], rows, sink, c.p.scale)
+            # the weights' and the result's bf16 rounding, 2^-8 each, and the logits' error
+            # (2 A scale |q|.|row| 2^-14, below 2^-8 A at these sizes)
+            assert np.all(np.abs(f64(c.out[c.cu[s] + i]) - o) <= 2.0 ** -8 * (2 * A + np.abs(o)))
+
+
+def test_cache_and_attention_past_32_bits():
+    """Pages whose rows start beyond 2^31 elements (4 GiB of bf16): written, read, attended to."""
+    pages = (1 << 31) // (512 * PE) + 3
+    kv_rows = torch.empty((pages * PE, 512), dtype=torch.bfloat16, device="cuda")
+    bt = i32([[pages - 1, pages - 2, 0]])
+    kv = L.kv_cache(L.CSA_BF16, 512, 0, kv_rows, None, None, bt)
+    x = randn(1, (600, 512), torch.bfloat16)
+    L.csa_cache_write(kv, L.CSA_BF16, x, i32([0, 600]), i32([0]), 1, 600)
+    assert torch.equal(kv_rows[(pages - 1) * PE:], x[:256])
+    out = torch.empty((1, 600, 512), dtype=torch.bfloat16, device="cuda")
+    L.csa_cache_read(kv, None, None, 1, 600, L.CSA_BF16, out)
+    assert torch.equal(out[0], x)
+    # the same rows in a small pool give the same attention, bit for bit
+    small = L.kv_cache(L.CSA_BF16, 512, 0, torch.zeros((3 * PE, 512), dtype=torch.bfloat16, device="cuda"), None,
+                       None, i32([[2, 0, 1]]))
+    L.csa_cache_write(small, L.CSA_BF16, x, i32([0, 600]), i32([0]), 1, 600)
+    p = L.AttnParams(H=64, d=512, n_w=128, scale=1.0 / math.sqrt(512), m=4, k=0, dtype=L.CSA_BF16)
+    res = []
+    for c in (kv, small):
+        for n in (5, 310):                           # split rows, and one CTA a token
+            q, nw, win = (randn(2, (n, 64, 512), torch.bfloat16), randn(3, (n, 512), torch.bfloat16),
+                          randn(4, (1, 128, 512), torch.bfloat16))
+            o = torch.empty_like(q)
+            ws = torch.empty(max(16, L.csa_chunk_attn_workspace_size(p, c, 1, n, 2400)), dtype=torch.uint8,
+                             device="cuda")
+            L.csa_chunk_attn(p, c, q, i32([0, n]), i32([2400 - n]), None, None, win, nw, randn(5, (64,)), 1, n,
+                             2400, o, None, ws)
+            res.append(o)
+    assert torch.equal(res[0], res[2]) and torch.equal(res[1], res[3])
+
+
+def test_chunk_attn_workspace_is_checked():
+    c = Case([3], [5000], m=4, k=512, fmt=L.CSA_BF16, seed=81, **TC)
+    need = L.csa_chunk_attn_workspace_size(c.p, c.kv, c.b, c.N, c.L_max)
+    assert need > 0 and L.csa_chunk_attn_launch_count(c.p, c.kv, c.b, c.N, c.L_max) == 2
+    args = (c.p, c.kv, c.q, i32(c.cu), i32(c.ctx), c.idx, c.count, c.win, c.new_win, c.sink, c.b, c.N, c.L_max,
+            c.out, c.lse)
+    for ws in (None, torch.empty(need - 1, dtype=torch.uint8, device="cuda"),
+               torch.empty(need + 16, dtype=torch.uint8, device="cuda")[4:]):
+        with pytest.raises(L.CsaError):
+            L.csa_chunk_attn(*args, ws)
+    with pytest.raises(L.CsaError):                  # a type, a size, a table too short, a place
+        L.csa_chunk_attn(*args[:2], c.q.float(), *args[3:], c.ws)
+    with pytest.raises(L.CsaError):
+        L.csa_chunk_attn(*args[:2], c.q[:-1], *args[3:], c.ws)
+    with pytest.raises(L.CsaError):
+        L.csa_cache_read(c.kv, None, None, 2, 4, L.CSA_BF16, torch.empty((2, 4, 512), dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(L.CsaError):
+        L.csa_cache_read(c.kv, None, None, 1, 4, L.CSA_BF16, torch.empty((1, 4, 512), dtype=torch.bfloat16))
+    assert torch.all(c.out == 7.0)
+
+
+def _steps(c):
+    """The five calls on one case's tensors (outputs of the case's shapes)."""
+    def run():
+        L.csa_qk_norm_rope(c.np_, c.q, None, c.new_win, None, c.pos, c.N, c.q2, c.w2)
+        L.csa_cache_write(c.kv, L.CSA_BF16, c.rows_in, c.wcu, c.wfirst, c.b, c.rows_in.shape[0])
+        L.csa_chunk_attn(c.p, c.kv, c.q2, c.dcu, c.dctx, None, None, c.win, c.w2, c.sink, c.b, c.N, c.L_max, c.out,
+                         c.lse, c.ws)
+        L.csa_window_append(L.CSA_BF16, c.d, c.n_w, c.win2, c.w2, c.dcu, c.dctx, c.b, c.N)
+        L.csa_cache_read(c.kv, None, None, c.b, 64, L.CSA_BF16, c.back)
+    return run
+
+
+def _step_case(seed, fmt, d_hi):
+    c = Case([5, 33], [1000, 40], m=4, k=0, fmt=fmt, d_hi=d_hi, d_rope_out=64, seed=seed, **TC)
+    c.np_ = L.NormRopeParams(H=64, d=512, d_rope=64, rope_theta=THETA, eps=EPS, apply_norm=1, dtype=L.CSA_BF16)
+    c.pos = i32([1000 + i for i in range(5)] + [40 + i for i in range(33)] + [0] * (c.N - 38))
+    c.q2, c.w2, c.win2 = torch.zeros_like(c.q), torch.zeros_like(c.new_win), c.win.clone()
+    c.rows_in = randn(seed + 9, (12, 512), torch.bfloat16)
+    c.wcu, c.wfirst = i32([0, 4, 12]), i32([246, 10])
+    c.dcu, c.dctx = i32(c.cu), i32(c.ctx)
+    c.back = torch.zeros((2, 64, 512), dtype=torch.bfloat16, device="cuda")
+    return c
+
+
+def _results(c):
+    return [x.clone() for x in (c.q2, c.w2, c.out, c.lse, c.win2, c.back)]
+
+
+@pytest.mark.parametrize("fmt,d_hi", [(L.CSA_BF16, 0), (L.CSA_FP8_E4M3, 64)])
+def test_captured_calls_follow_their_tensors(fmt, d_hi):
+    """A captured sequence of the calls, replayed on other values in the same tensors, gives what
+    the calls give on those values."""
+    a, b = _step_case(91, fmt, d_hi), _step_case(92, fmt, d_hi)
+    run = _steps(a)
+    run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    names = ("q", "new_win", "win", "win2", "sink", "rows_in", "pos", "dcu", "dctx", "wcu", "wfirst")
+    b.dcu, b.dctx = i32([0, 30, 38]), i32([77, 1300])          # other lengths and positions too
+    b.wfirst = i32([3, 300])
+    for n in names:
+        getattr(a, n).copy_(getattr(b, n))
+    # the other case's pages and table
+    for x, y in zip(a.kv._tensors, b.kv._tensors):
+        if x is not None:
+            x.copy_(y)
+    for x in (a.out, a.lse):
+        x.fill_(7.0)
+    g.replay()
+    torch.cuda.synchronize()
+    got = _results(a)
+    _steps(b)()
+    torch.cuda.synchronize()
+    for x, y in zip(got, _results(b)):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("fmt,d_hi", [(L.CSA_BF16, 0), (L.CSA_FP8_E4M3, 64)])
+def test_two_streams_at_once(fmt, d_hi):
+    """Two independent sequences of the calls on two streams, many times over, and the same on one
+    stream: the same bits (no state shared between calls)."""
+    a, b = _step_case(101, fmt, d_hi), _step_case(102, fmt, d_hi)
+    want = []
+    for c in (a, b):
+        _steps(c)()
+        torch.cuda.synchronize()
+        want.append(_results(c))
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(20):
+        for c, s in ((a, s1), (b, s2)):
+            with torch.cuda.stream(s):
+                _steps(c)()
+    torch.cuda.synchronize()
+    assert L.csa_device_error() == 0
+    for c, w in zip((a, b), want):
+        for x, y in zip(_results(c), w):
+            assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("fmt", [L.CSA_BF16, L.CSA_FP8_E4M3])
+@pytest.mark.parametrize("m,n", [(4, 700), (128, 1500)])
+def test_a_sequence_served_in_chunks(fmt, m, n):
+    """A prompt brought in chunks of every size, its entries compressed, written to pages and
+    attended to chunk by chunk, against one dense call over the whole sequence.
+
+    Tolerance: both calls round their weights (2^-8) and results (2^-8) to bf16, so they differ by
+    at most twice 2^-8 (A + |o|) with A = sum w |row| <= max |row| over the sequence's rows; the
+    float32 parts are far below.  A is taken from the whole call's rows."""
+    d, H, n_w = 512, 64, 128
+    raw = {k: randn(i, (1, n, d), torch.bfloat16) for i, k in enumerate(("C", "Z"))}
+    Bp = randn(7, (m, d))
+    E = n // m
+    cp = L.CompressParams(m=m, overlap=0, c=d, d_rope=64, rope_theta=THETA, eps=EPS, apply_norm=1,
+                          in_dtype=L.CSA_BF16, out_dtype=L.CSA_BF16, out_entry_offset=0)
+    ent = torch.zeros((1, E, d), dtype=torch.bfloat16, device="cuda")
+    L.csa_compress(cp, raw["C"], raw["Z"], Bp, None, None, None, 1, n, 0, E, E, ent)
+    qraw, kraw = randn(8, (n, H, d), torch.bfloat16), raw["C"][0]
+    nrm = L.NormRopeParams(H=H, d=d, d_rope=64, rope_theta=THETA, eps=EPS, apply_norm=1, dtype=L.CSA_BF16)
+    sink = randn(9, (H,))
+    pages = -(-E // PE) + 1
+    bt = i32([[(3 * j + 1) % pages if pages % 3 else j for j in range(-(-E // PE))]])
+    kv = L.alloc_kv_cache(fmt, d, 64 if fmt == L.CSA_FP8_E4M3 else 0, pages, bt)
+    win = torch.zeros((1, n_w, d), dtype=torch.bfloat16, device="cuda")
+    p = L.AttnParams(H=H, d=d, n_w=n_w, scale=1.0 / math.sqrt(d), m=m, k=0, dtype=L.CSA_BF16, d_rope_out=64,
+                     rope_theta=THETA)
+    q_all, w_all = torch.empty_like(qraw), torch.empty_like(kraw)
+    outs, lses, at = [], [], 0
+    for size in (1, 2, 37, 128, 300, n):
+        size = min(size, n - at)
+        if not size:
+            break
+        pos = torch.arange(at, at + size, dtype=torch.int32, device="cuda")
+        q, w = q_all[at:at + size], w_all[at:at + size]
+        L.csa_qk_norm_rope(nrm, qraw[at:at + size], None, kraw[at:at + size], None, pos, size, q, w)
+        e0, e1 = at // m, (at + size) // m           # the entries this chunk completes
+        if e1 > e0:
+            L.csa_cache_write(kv, L.CSA_BF16, ent[0, e0:e1], i32([0, e1 - e0]), i32([e0]), 1, e1 - e0)
+        o, l = torch.empty_like(q), torch.empty((size, H), device="cuda")
+        ws = torch.empty(max(16, L.csa_chunk_attn_workspace_size(p, kv, 1, size, at + size)), dtype=torch.uint8,
+                         device="cuda")
+        L.csa_chunk_attn(p, kv, q, i32([0, size]), i32([at]), None, None, win, w, sink, 1, size, at + size, o, l, ws)
+        L.csa_window_append(L.CSA_BF16, d, n_w, win, w, i32([0, size]), i32([at]), 1, size)
+        outs.append(o)
+        lses.append(l)
+        at += size
+    # the whole sequence at once, over the rows the cache stands for
+    rows = torch.empty((1, E, d), dtype=torch.bfloat16, device="cuda")
+    L.csa_cache_read(kv, None, None, 1, E, L.CSA_BF16, rows)
+    if fmt == L.CSA_BF16:
+        assert torch.equal(rows, ent)
+    out, lse = torch.empty((1, n, H, d), dtype=torch.bfloat16, device="cuda"), torch.empty((1, n, H), device="cuda")
+    wsz = L.csa_sparse_attn_workspace_size(p, 1, n, E)
+    L.csa_sparse_attn(p, q_all[None], rows, E, None, None, w_all[None].contiguous(), n,
+                      torch.arange(n, dtype=torch.int32, device="cuda")[None], sink, 1, n, out, lse,
+                      torch.empty(max(16, wsz), dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    assert L.csa_device_error() == 0
+    A = max(float(rows.abs().max()), float(w_all.abs().max())) * math.sqrt(2.0)   # a rotated pair mixes
+    err = (torch.cat(outs).float() - out[0].float()).abs().max()
+    assert float(err) <= 2 * 2.0 ** -8 * 2 * A
+    # the lse: the whole call sums rounded weights (2^-8 each, relative)
+    assert float((torch.cat(lses) - lse[0]).abs().max()) <= 2.0 ** -8 + 2.0 ** -14 * 100
