@@ -32,7 +32,8 @@
 // register shares go by warpgroup).
 // Producers walk the CTA's tiles as one stream across its items.
 //
-// Work item = (token, split of its tiles); CTAs walk the items with stride gridDim.x.  Few
+// Work item = (token, split of its tiles); CTAs walk the items with stride gridDim.x, the
+// longest sequences' first.  Few
 // tokens are split over several CTAs (fp32 partials, combined by chunk_merge_kernel), many
 // are not.  The rows' addresses come from a chain of loads (selection -> block table ->
 // row), run two tiles ahead of their use.
@@ -72,6 +73,7 @@ static_assert(kRegsSoftmax <= kRegsLaunch && kRegsProd >= kRegsLaunch && kRegsMm
                   2 * kRegsSoftmax + 2 * kRegsProd + kRegsMma <= 5 * kRegsLaunch, "setmaxnreg shares");
 constexpr uint32_t kHintNs = 64;
 constexpr int kSeqCache = 1024;       // sequences whose boundaries are kept in shared memory
+constexpr int kSeqOrder = 64;         // sequences that are taken in order of length
 constexpr int kMaxSplit = 32;
 constexpr int kNewTag = 1 << 30;      // window rows: new_win's row + kNewTag, or the rings' row
 
@@ -84,30 +86,58 @@ struct ChunkTc {
   float *part_o, *part_m, *part_l;   // per item [64][512], [64], [64]
   int* err;
   csa_kv_cache kv;
-  int b, N, n_w, m, k, nsplit, items, d_rope_out;
+  int b, N, n_w, m, k, nsplit, items, order, d_rope_out;
   float scale_log2;
   double inv_freq[kMaxOutRopePairs];
 };
 
 struct Item {
-  int tok, seq, i0, p0, t, nsel, ne, w0, tb, te;
+  int tok, part, seq, i0, p0, t, nsel, ne, w0, tb, te;   // part: tok * nsplit + split
   bool live;
 };
 
-// Item `item` (whole warp).  cu / pos0 point to shared or global memory.
-__device__ __forceinline__ Item get_item(const ChunkTc& p, const int32_t* cu, const int32_t* pos0,
-                                         int item, int lane) {
+// The sequences as the CTAs walk them: boundaries and first positions (in shared memory where
+// they fit), and, where the sequences are taken longest first, their order and the boundaries
+// in that order.
+struct Seqs {
+  const int32_t* s;        // shared memory: cu [kSeqCache + 1], pos0 [kSeqCache], cum, ord
+  bool cached, ordered;
+  __device__ __forceinline__ const int32_t* cu(const ChunkTc& p) const { return cached ? s : p.cu_q; }
+  __device__ __forceinline__ const int32_t* pos0(const ChunkTc& p) const {
+    return cached ? s + kSeqCache + 1 : p.pos0;
+  }
+  __device__ __forceinline__ const int32_t* cum(const ChunkTc& p) const {
+    return ordered ? s + 2 * kSeqCache + 1 : cu(p);
+  }
+  __device__ __forceinline__ int seq(int j) const {
+    return ordered ? s[2 * kSeqCache + 1 + kSeqOrder + 1 + j] : j;
+  }
+};
+
+// The n-th item of this CTA.  In order of length, every other round runs the other way, so that
+// the CTA with the longest items of one round has the shortest of the next.
+__device__ __forceinline__ int item_at(const Seqs& q, int n) {
+  const int x = q.ordered && (n & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+  return n * gridDim.x + x;
+}
+
+// Item `item` (whole warp).
+__device__ __forceinline__ Item get_item(const ChunkTc& p, const Seqs& q, int item, int lane) {
   Item I;
-  I.tok = item / p.nsplit;
-  const int split = item - I.tok * p.nsplit;
-  I.seq = find_seq(cu, p.b, I.tok, lane);
-  I.live = I.seq < p.b && I.tok >= cu[0];
+  const int rank = item / p.nsplit;
+  const int split = item - rank * p.nsplit;
+  const int32_t* cum = q.cum(p);
+  const int j = find_seq(cum, p.b, rank, lane);
+  I.live = j < p.b && rank >= cum[0];
   if (!I.live) {
-    I.i0 = I.p0 = I.t = I.nsel = I.ne = I.w0 = I.tb = I.te = 0;
+    I.tok = I.part = I.seq = I.i0 = I.p0 = I.t = I.nsel = I.ne = I.w0 = I.tb = I.te = 0;
     return I;
   }
-  I.i0 = cu[I.seq];
-  I.p0 = pos0[I.seq];
+  I.seq = q.seq(j);
+  I.i0 = q.cu(p)[I.seq];
+  I.tok = I.i0 + (rank - cum[j]);
+  I.part = I.tok * p.nsplit + split;
+  I.p0 = q.pos0(p)[I.seq];
   I.t = I.p0 + (I.tok - I.i0);
   int ns = 0, nwin = 0;
   I.w0 = 0;
@@ -127,15 +157,14 @@ __device__ __forceinline__ Item get_item(const ChunkTc& p, const int32_t* cu, co
 // The tiles of a CTA's items, one after another (empty items skipped).
 struct Stream {
   Item it;
-  int item, tile;
+  int n, tile;   // item_at(n)
   bool live;
 };
-__device__ __forceinline__ void stream_settle(Stream& s, const ChunkTc& p, const int32_t* cu,
-                                              const int32_t* pos0, int lane) {
+__device__ __forceinline__ void stream_settle(Stream& s, const ChunkTc& p, const Seqs& q, int lane) {
   while (s.live && s.tile >= s.it.te) {
-    s.item += gridDim.x;
-    if (s.item >= p.items) { s.live = false; break; }
-    s.it = get_item(p, cu, pos0, s.item, lane);
+    const int item = item_at(q, ++s.n);
+    if (item >= p.items) { s.live = false; break; }
+    s.it = get_item(p, q, item, lane);
     s.live = s.it.live;
     s.tile = s.it.tb;
   }
@@ -436,6 +465,8 @@ __global__ void __launch_bounds__(kLaunch, 1)
   uint16_t* s_valid16 = reinterpret_cast<uint16_t*>(s_valid);   // ... as the producers write them
   int32_t* s_cu = reinterpret_cast<int32_t*>(s_valid + 4);   // [kSeqCache + 1]
   int32_t* s_pos0 = s_cu + kSeqCache + 1;         // [kSeqCache]
+  int32_t* s_cum = s_pos0 + kSeqCache;            // [kSeqOrder + 1]
+  int32_t* s_ord = s_cum + kSeqOrder + 1;         // [kSeqOrder]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
@@ -444,8 +475,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
     for (int i = tid; i <= p.b; i += kLaunch) s_cu[i] = p.cu_q[i];
     for (int i = tid; i < p.b; i += kLaunch) s_pos0[i] = p.pos0[i];
   }
-  const int32_t* cu = cached ? s_cu : p.cu_q;
-  const int32_t* pos0 = cached ? s_pos0 : p.pos0;
+  Seqs seqs{s_cu, cached, false};
   if (tid < kH) s_sink2[tid] = p.sink[tid] * kLog2e;
   if (tid == 0) {
     tc::mbar_init(bar_s, 1);
@@ -458,6 +488,31 @@ __global__ void __launch_bounds__(kLaunch, 1)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  if (p.order && s_cu[p.b] <= p.N) {               // (uniform; b fits the cached part)
+    // rank of a sequence by the entries its last token sees, longest first
+    const int s = tid;
+    if (s < p.b) {
+      auto rows = [&](int x) {
+        const int e = max(0, (s_pos0[x] + (s_cu[x + 1] - s_cu[x])) / p.m);
+        return p.idx ? min(e, p.k) : e;
+      };
+      const int mine = rows(s);
+      int r = 0;
+      for (int x = 0; x < p.b; ++x) {
+        const int other = rows(x);
+        r += other > mine || (other == mine && x < s);
+      }
+      s_ord[r] = s;
+    }
+    __syncthreads();
+    if (tid <= p.b) {
+      int c = 0;
+      for (int x = 0; x < tid; ++x) c += s_cu[s_ord[x] + 1] - s_cu[s_ord[x]];
+      s_cum[tid] = c;
+    }
+    __syncthreads();
+    seqs.ordered = true;
+  }
   const uint32_t tS = tmem, tO = tmem + 64;       // columns [0, 64) S^T; [64, 320) O^T
 
   if (warp >= kSW + kPW) {
@@ -470,8 +525,8 @@ __global__ void __launch_bounds__(kLaunch, 1)
     const uint64_t dS_b = tc::smem_desc_sw128(tc::smem_u32(sQ), 16, 1024);
     const uint64_t dO_a = tc::smem_desc_sw128(tc::smem_u32(sKV), kKVBlk, 1024);
     const uint64_t dO_b = tc::smem_desc_sw128(tc::smem_u32(sP), 8192, 1024);
-    for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
-      const Item I = get_item(p, cu, pos0, item, lane);
+    for (int n = 0, item; (item = item_at(seqs, n)) < p.items; ++n) {
+      const Item I = get_item(p, seqs, item, lane);
       if (!I.live) break;
       for (int j = I.tb; j < I.te; ++j) {
 #pragma unroll 1
@@ -514,14 +569,14 @@ __global__ void __launch_bounds__(kLaunch, 1)
     // run ahead: a pair of the next tile lands after this tile's PV has read its place.)
     if (warp == kSW + kPW + 1) {
       bool ok = true;
-      uint32_t n = 0;
-      for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
-        const Item I = get_item(p, cu, pos0, item, lane);
+      uint32_t g = 0;
+      for (int n = 0, item; (item = item_at(seqs, n)) < p.items; ++n) {
+        const Item I = get_item(p, seqs, item, lane);
         if (!I.live) break;
-        for (int j = I.tb; j < I.te; ++j, ++n) {
+        for (int j = I.tb; j < I.te; ++j, ++g) {
 #pragma unroll 1
           for (int mb = 0; mb < 4; ++mb) {
-            ok = ok && tc::mbar_wait_hint(bar_full + mb, n & 1, p.err, kHintNs);
+            ok = ok && tc::mbar_wait_hint(bar_full + mb, g & 1, p.err, kHintNs);
             tc::named_bar_arrive(4 + mb, kBarW);
           }
         }
@@ -539,14 +594,14 @@ __global__ void __launch_bounds__(kLaunch, 1)
     uint2 sc = make_uint2(0u, 0u);                 // FP8: the scales of this lane's row, and the
     int c4[4];                                     // numbers of the four rows it loads
     Stream S;
-    S.item = blockIdx.x;
-    S.live = S.item < p.items;
+    S.n = 0;
+    S.live = item_at(seqs, 0) < p.items;
     S.it.te = S.tile = 0;
     if (S.live) {
-      S.it = get_item(p, cu, pos0, S.item, lane);
+      S.it = get_item(p, seqs, item_at(seqs, 0), lane);
       S.live = S.it.live;
       S.tile = S.it.tb;
-      stream_settle(S, p, cu, pos0, lane);
+      stream_settle(S, p, seqs, lane);
     }
     // the first tile's row numbers, loads and queries, then the second tile's rows
     RowRef nx;
@@ -561,8 +616,8 @@ __global__ void __launch_bounds__(kLaunch, 1)
       if (!live) return;
       code = row_code(nx, p);
       window = nx.window;
-      new_q = S.item != item;
-      item = S.item;
+      new_q = S.n != item;
+      item = S.n;
       have = __ballot_sync(0xffffffffu, code >= 0);
       // 128 consecutive rows of one page that all exist come by TMA, straight into the tile
       whole = !FP8 && !window && !p.idx && (S.tile + 1) * kRows <= S.it.nsel && have == 0xffffffffu;
@@ -575,7 +630,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
       }
       if (!new_q) {
         ++S.tile;
-        stream_settle(S, p, cu, pos0, lane);
+        stream_settle(S, p, seqs, lane);
         row_entry(nx, S, p, myrow);
       }
     };
@@ -583,7 +638,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
       if (!live || !new_q) return;
       load_q(p, S.it.tok, sQ, w, lane);
       ++S.tile;
-      stream_settle(S, p, cu, pos0, lane);
+      stream_settle(S, p, seqs, lane);
       row_entry(nx, S, p, myrow);
     };
     take();
@@ -681,8 +736,8 @@ __global__ void __launch_bounds__(kLaunch, 1)
     uint32_t ns = 0;                               // tiles so far
     bool ok = true;
 
-    for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
-      const Item I = get_item(p, cu, pos0, item, lane);
+    for (int n = 0, item; (item = item_at(seqs, n)) < p.items; ++n) {
+      const Item I = get_item(p, seqs, item, lane);
       if (!I.live) break;
       bool started = false;                        // a tile of this item had a row
       float lsum[8], ref[8];                       // sums, and reference maxima (log2 units, 0: none)
@@ -817,8 +872,8 @@ __global__ void __launch_bounds__(kLaunch, 1)
       if (I.te <= I.tb) {
         if (p.nsplit > 1) {                        // nothing to add: weight 0, O not written
           if (tid < kH) {
-            p.part_m[(long long)item * kH + tid] = -INFINITY;
-            p.part_l[(long long)item * kH + tid] = 0.f;
+            p.part_m[(long long)I.part * kH + tid] = -INFINITY;
+            p.part_l[(long long)I.part * kH + tid] = 0.f;
           }
         } else {
           uint4* o = reinterpret_cast<uint4*>(p.out + (long long)I.tok * kH * kD);
@@ -843,8 +898,8 @@ __global__ void __launch_bounds__(kLaunch, 1)
         const float l = s_red[tid] + s_red[kH + tid] + s_red[2 * kH + tid] + s_red[3 * kH + tid];
         const float M = s_M[tid];
         if (p.nsplit > 1) {
-          p.part_m[(long long)item * kH + tid] = M;
-          p.part_l[(long long)item * kH + tid] = l;
+          p.part_m[(long long)I.part * kH + tid] = M;
+          p.part_l[(long long)I.part * kH + tid] = l;
         } else {
           const float sink2 = s_sink2[tid], top = fmaxf(M, sink2);
           const float wr = rel_weight(M, top);
@@ -863,7 +918,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
           uint32_t o[32];
           tc::tmem_ld32(tO + mb * kH + 32 * hf + lane_addr, o);
           tc::tmem_ld_wait(o);
-          float* dst = p.part_o + ((long long)item * kH + 32 * hf) * kD + mb * 128 + row;
+          float* dst = p.part_o + ((long long)I.part * kH + 32 * hf) * kD + mb * 128 + row;
 #pragma unroll
           for (int h = 0; h < 32; ++h) dst[h * kD] = ok ? __uint_as_float(o[h]) : nan_f();
         }
@@ -972,7 +1027,7 @@ __global__ void __launch_bounds__(128 * kMergeHeads) chunk_merge_kernel(const __
 }
 
 constexpr size_t kSmem = 1024 + 8 * kKVBlk + 8 * kQBlk + kRows * 128 + (4 * kH + 3 * kH) * 4 + 16 + 9 * 8 + 8 + 16 +
-                         (2 * kSeqCache + 1) * 4;
+                         (2 * kSeqCache + 1 + 2 * kSeqOrder + 1) * 4;
 static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 
 int sm_count() {
@@ -1037,7 +1092,7 @@ csa_status launch_chunk_attn_tc(const ChunkArgs& a, const csa_kv_cache& kv, void
     p.inv_freq[j] = 2 * j < a.d_rope_out ? std::pow(a.theta, -2.0 * j / (double)a.d_rope_out) : 0.0;
   p.nsplit = plan_splits(a.n_w, a.m, a.k, a.N, a.L_max);
   const long long items = (long long)a.N * p.nsplit;
-  if (items > INT_MAX) return CSA_ERR_UNSUPPORTED;
+  if (items > INT_MAX - (1 << 20)) return CSA_ERR_UNSUPPORTED;   // a round past the last fits too
   p.items = (int)items;
   if (p.nsplit > 1) {
     if (!ws || ws_bytes < (size_t)items * kH * (kD + 2) * 4 || (reinterpret_cast<uintptr_t>(ws) & 15))
@@ -1055,6 +1110,10 @@ csa_status launch_chunk_attn_tc(const ChunkArgs& a, const csa_kv_cache& kv, void
       !make_tmap_2d_b16(&tm, kv.rows, kD, (uint64_t)kv.num_pages * kPageEntries, 64, kRows))
     return CSA_ERR_CUDA;
   const int grid = (int)std::min<long long>(items, sm_count());
+  // Several rounds of items of several sequences: longest first, so that no CTA meets a long
+  // token last.  (One token of 44 tiles before 927 of 1 to 17: 431 us in the given order, 300 in
+  // this; more sequences than kSeqOrder even out by themselves, and sorting them would take long.)
+  p.order = p.items > grid && a.b > 1 && a.b <= kSeqOrder;
   if (csa_launch(kern, dim3(grid), dim3(kLaunch), kSmem, st, false, tm, p) != cudaSuccess) return CSA_ERR_CUDA;
   if (p.nsplit > 1 &&
       csa_launch(chunk_merge_kernel, dim3(a.N, kH / kMergeHeads), dim3(128 * kMergeHeads), 0, st, true, p) != cudaSuccess)
