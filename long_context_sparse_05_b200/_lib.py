@@ -442,8 +442,8 @@ def _arg(x, dtype, what, numel, dev):
     device dev; None stays None."""
     if x is None:
         return None
-    if (x.dtype is dtype and x.is_cuda and x.get_device() == dev and x.is_contiguous() and
-            x.numel() >= numel):
+    # (a CPU tensor's device number is -1)
+    if x.dtype is dtype and x.get_device() == dev and x.is_contiguous() and x.numel() >= numel:
         return x.data_ptr()
     why = _bad(x, dtype, what, numel, dev)
     if why:

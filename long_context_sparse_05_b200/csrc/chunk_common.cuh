@@ -2,6 +2,8 @@
 // sequence a ragged row belongs to, and where an entry lives.
 #pragma once
 
+#include <cmath>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -26,6 +28,14 @@ __device__ __forceinline__ long long page_row(const csa_kv_cache& kv, int s, lon
   const int pg = kv.block_table[(size_t)s * kv.max_pages + (size_t)(e / kPageEntries)];
   if ((unsigned)pg >= (unsigned)kv.num_pages) return -1;
   return (long long)pg * kPageEntries + (e % kPageEntries);
+}
+
+// Host: theta^(-2j/d_rope) for the d_rope / 2 rotary pairs, as powers of one root in extended
+// precision (a call of pow for each pair was a microsecond of every small call).
+inline void rope_frequencies(double* f, int d_rope, double theta) {
+  const long double root = d_rope > 0 ? powl((long double)theta, -2.0L / d_rope) : 0.0L;
+  long double x = 1.0L;
+  for (int j = 0; 2 * j < d_rope; ++j, x *= root) f[j] = (double)x;
 }
 
 // The value of scale byte e: 2^(e - 127) (the byte is a float's exponent field).

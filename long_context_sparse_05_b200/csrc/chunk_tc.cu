@@ -42,7 +42,6 @@
 
 #include <algorithm>
 #include <climits>
-#include <cmath>
 
 namespace csa {
 
@@ -1088,8 +1087,7 @@ csa_status launch_chunk_attn_tc(const ChunkArgs& a, const csa_kv_cache& kv, void
   p.scale_log2 = a.scale * kLog2e;
   p.err = device_error_word();
   if (!p.err) return CSA_ERR_CUDA;
-  for (int j = 0; j < kMaxOutRopePairs; ++j)
-    p.inv_freq[j] = 2 * j < a.d_rope_out ? std::pow(a.theta, -2.0 * j / (double)a.d_rope_out) : 0.0;
+  rope_frequencies(p.inv_freq, a.d_rope_out, a.theta);
   p.nsplit = plan_splits(a.n_w, a.m, a.k, a.N, a.L_max);
   const long long items = (long long)a.N * p.nsplit;
   if (items > INT_MAX - (1 << 20)) return CSA_ERR_UNSUPPORTED;   // a round past the last fits too

@@ -13,7 +13,6 @@
 // four CTAs an SM; short ones (too few rows for that to fill the SMs) take one.  4096 tokens
 // of 64 heads of 512 (545 MB): 109 us, 5.0 TB/s (one row per warp 137 us, two 114, four
 // without the register bound 117); 16 tokens: 3.2 us.
-#include <cmath>
 
 #include "chunk_common.cuh"
 
@@ -193,8 +192,7 @@ csa_status launch_t(const NormRopeArgs& a, long long rows, cudaStream_t st) {
 }  // namespace
 
 csa_status launch_norm_rope(NormRopeArgs& a, int dtype, double theta, cudaStream_t st) {
-  for (int j = 0; j < kMaxRopePairs; ++j)
-    a.inv_freq[j] = 2 * j < a.d_rope ? std::pow(theta, -2.0 * j / (double)a.d_rope) : 0.0;
+  rope_frequencies(a.inv_freq, a.d_rope, theta);
   const long long rows = (long long)a.N * ((a.q ? a.H : 0) + (a.kv ? 1 : 0));
   if (rows > 0x7fffffffLL - 64) return CSA_ERR_UNSUPPORTED;
   return dtype == CSA_F32 ? launch_t<float>(a, rows, st) : launch_t<__nv_bfloat16>(a, rows, st);
