@@ -488,6 +488,8 @@ def kv_cache(dtype, c, d_hi, rows, hi, scales, block_table):
         raise CsaError("hi and scales belong to an FP8 cache")
     stride = ((c - d_hi) // SCALE_GROUP + 7) // 8 * 8
     dev = rows.get_device()
+    if dev < 0:
+        raise CsaError("tensor arguments must be CUDA tensors (rows is on %s)" % rows.device)
     kv = KVCache(dtype=dtype, c=c, d_hi=d_hi, num_pages=pages, max_pages=block_table.shape[1],
                  rows=_arg(rows, _ELEM[dtype], "rows", 0, dev),
                  hi=_arg(hi, torch.bfloat16, "hi", n * d_hi, dev),
