@@ -16,11 +16,15 @@
 // of operands, 48 cycles at 128 bytes a cycle, for 32 cycles of math), and one tile of
 // shared memory (128 KB, beside 64 KB of queries) leaves no room for a second.  So the next
 // tile waits in registers: producer warps issue its loads as soon as the current tile is
-// stored (two of its four 128-dim pairs in bf16, three in FP8), they travel under this
-// tile's softmax and PV, and each pair is stored the moment the PV has read its predecessor;
-// its S^T MMAs start on it.  FP8 rows become bf16 on the way to shared memory (code times a
-// power of two: exact).  Loads and softmax in the same warps made a tile 10,400 cycles, since
-// the softmax's shuffles and shared-memory accesses queued behind the loads.
+// stored, they travel under this tile's softmax and PV, and each 128-dim pair is stored the
+// moment the PV has read its predecessor; its S^T MMAs start on it.  FP8 rows become bf16 on
+// the way to shared memory (code times a power of two: exact).  A whole tile of neighbouring
+// bf16 rows needs no registers: TMA puts each pair in place as soon as that is free.  Chosen
+// rows go through registers, since row gathers by TMA (one row of 128 bytes after another)
+// moved 9 to 25 bytes a cycle and SM against 55 to 80.  A dense bf16 tile takes ~6,100 cycles,
+// one of FP8 ~7,500.  Measured and not taken: loads and softmax in the same warps (10,400
+// cycles: the softmax's shuffles and shared-memory accesses queue behind the loads), and two
+// tiles of 64 rows in turn (M = 64 halves the MMA's rate: a dense chunk 27 % slower).
 //
 // The softmax keeps the maximum lazily (raised only when a tile exceeds it by 2^8, which
 // rescales O^T in TMEM) and each thread's sums of its 32 heads in registers over the tiles of
@@ -33,10 +37,9 @@
 // Producers walk the CTA's tiles as one stream across its items.
 //
 // Work item = (token, split of its tiles); CTAs walk the items with stride gridDim.x, the
-// longest sequences' first.  Few
-// tokens are split over several CTAs (fp32 partials, combined by chunk_merge_kernel), many
-// are not.  The rows' addresses come from a chain of loads (selection -> block table ->
-// row), run two tiles ahead of their use.
+// longest sequences' first.  Few tokens are split over several CTAs (fp32 partials, combined
+// by chunk_merge_kernel), many are not.  The rows' addresses come from a chain of loads
+// (selection -> block table -> row), run two tiles ahead of their use.
 #include "chunk_common.cuh"
 #include "tc_common.cuh"
 
@@ -235,6 +238,7 @@ template <bool FP8> constexpr int kPairs = FP8 ? 2 : 3;
 //
 // bf16 rows: kPairs of a tile's four pairs are staged; the others are loaded into their
 // registers as those are stored.
+
 // Numbers of the four rows this lane loads.
 __device__ __forceinline__ void row_numbers(int (&c)[4], int code, int lane) {
 #pragma unroll
@@ -392,8 +396,8 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   if (lane == 0) tc::mbar_arrive(bar);
 }
 
-// 16 TMEM lanes x 32 columns: lane l gets TMEM lanes l / 4 and l / 4 + 8, columns 8 g + 2 (l % 4) and the next, as
-// r[4 g], r[4 g + 1] and r[4 g + 2], r[4 g + 3].
+// 16 TMEM lanes x 32 columns: lane l gets TMEM lanes l / 4 and l / 4 + 8, columns
+// 8 g + 2 (l % 4) and the next, as r[4 g], r[4 g + 1] and r[4 g + 2], r[4 g + 3].
 __device__ __forceinline__ void tmem_ld16(uint32_t ta, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
@@ -779,6 +783,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
           exact = tc::bar_red_or(3, kST, top > kRescale);
         }
         if (exact) {
+          const bool rows = (s_valid[0] | s_valid[1] | s_valid[2] | s_valid[3]) != 0;
           float v[8];
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
@@ -804,7 +809,9 @@ __global__ void __launch_bounds__(kLaunch, 1)
           if (tid < kH) {
             // this tile's maxima, relative to the reference that the logits were taken against
             const float tm = fmaxf(fmaxf(s_red[tid], s_red[kH + tid]), fmaxf(s_red[2 * kH + tid], s_red[3 * kH + tid]));
-            float Mn = started ? s_M[tid] : tm, al = started ? 1.f : 0.f;
+            // (rows whose logits are all -inf are taken against 0: they weigh nothing)
+            float Mn = started ? s_M[tid] : rows && tm == -INFINITY ? 0.f : tm;
+            float al = started ? 1.f : 0.f;
             if (started && tm > kRescale) {
               Mn += tm;
               al = exp2f(-tm);
@@ -840,7 +847,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
             lsum[2 * g] *= a2.x;
             lsum[2 * g + 1] *= a2.y;
           }
-          started = s_M[0] != -INFINITY;           // rows are masked for all heads alike
+          started = started || rows;               // rows are masked for all heads alike
           logits();
           // nobody may overwrite these maxima before everyone has read them
           tc::named_bar(3, kST);
@@ -895,7 +902,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
       tc::named_bar(3, kST);
       if (tid < kH) {
         const float l = s_red[tid] + s_red[kH + tid] + s_red[2 * kH + tid] + s_red[3 * kH + tid];
-        const float M = s_M[tid];
+        const float M = l == 0.f ? -INFINITY : s_M[tid];
         if (p.nsplit > 1) {
           p.part_m[(long long)I.part * kH + tid] = M;
           p.part_l[(long long)I.part * kH + tid] = l;
@@ -1109,7 +1116,7 @@ csa_status launch_chunk_attn_tc(const ChunkArgs& a, const csa_kv_cache& kv, void
     return CSA_ERR_CUDA;
   const int grid = (int)std::min<long long>(items, sm_count());
   // Several rounds of items of several sequences: longest first, so that no CTA meets a long
-  // token last.  (One token of 44 tiles before 927 of 1 to 17: 431 us in the given order, 300 in
+  // token last.  (One token of 44 tiles before 927 of 1 to 17: 431 us in the given order, 310 in
   // this; more sequences than kSeqOrder even out by themselves, and sorting them would take long.)
   p.order = p.items > grid && a.b > 1 && a.b <= kSeqOrder;
   if (csa_launch(kern, dim3(grid), dim3(kLaunch), kSmem, st, false, tm, p) != cudaSuccess) return CSA_ERR_CUDA;

@@ -509,6 +509,34 @@ def test_chunk_attn_counts_out_of_range(fmt, d_hi, shape):
     c.check()
 
 
+@pytest.mark.parametrize("cfg", [
+    dict(TC, fmt=L.CSA_BF16, lens=[5, 3], ctx=[2500, 900]),          # split over several CTAs
+    dict(TC, fmt=L.CSA_BF16, lens=[300], ctx=[2500]),                # not split
+    dict(TC, fmt=L.CSA_FP8_E4M3, d_hi=64, lens=[300], ctx=[2500]),
+    dict(SMALL, lens=[5, 3], ctx=[2500, 900]),
+])
+def test_chunk_attn_a_head_of_infinities(cfg):
+    """Head 0's logits are all -inf: its sink takes all, and the other heads are untouched."""
+    c = Case(**dict(cfg, m=4, k=0, seed=81))
+    if c.fmt == L.CSA_FP8_E4M3:
+        c.kv._tensors[0].view(-1, c.d - c.d_hi)[:, 0] = 0x38         # 1.0
+    else:
+        c.kv._tensors[0].view(-1, c.d)[:, 0] = 1.0
+    c.win[..., 0] = 1.0
+    c.new_win[..., 0] = 1.0
+    finite = c.q.clone()
+    c.q[:, 0, 0] = -math.inf
+    c.run()
+    out, lse, n = c.out.clone(), c.lse.clone(), c.cu[-1]
+    assert torch.all(out[:n, 0] == 0)
+    s = c.sink[0].item()
+    assert torch.all((lse[:n, 0] - s).abs() <= 2.0 ** -20 + 2.0 ** -22 * abs(s))
+    c.q = finite
+    c.run()
+    c.out[:, 1:], c.lse[:, 1:] = out[:, 1:], lse[:, 1:]
+    c.check(tokens=5)
+
+
 @pytest.mark.parametrize("b", [33, 1100])
 def test_chunk_attn_many_sequences(b):
     """More sequences than one step of the search, and than shared memory holds."""
