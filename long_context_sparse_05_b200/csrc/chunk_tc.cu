@@ -396,35 +396,49 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   if (lane == 0) tc::mbar_arrive(bar);
 }
 
-// 16 TMEM lanes x 32 columns: lane l gets TMEM lanes l / 4 and l / 4 + 8, columns
-// 8 g + 2 (l % 4) and the next, as r[4 g], r[4 g + 1] and r[4 g + 2], r[4 g + 3].
-__device__ __forceinline__ void tmem_ld16(uint32_t ta, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(ta) : "memory");
-  asm volatile(
-      "tcgen05.wait::ld.sync.aligned;"
-      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-      :: "memory");
+// 32 TMEM lanes x 32 columns, as two pieces of 16 lanes: of piece y, lane l gets TMEM lanes
+// 16 y + l / 4 and 8 further, columns 8 g + 2 (l % 4) and the next, as r[y][4 g], r[y][4 g + 1]
+// and r[y][4 g + 2], r[y][4 g + 3].  One wait for both.
+__device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t (&r)[2][16]) {
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    uint32_t(&q)[16] = r[y];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]),
+          "=r"(q[7]), "=r"(q[8]), "=r"(q[9]), "=r"(q[10]), "=r"(q[11]), "=r"(q[12]), "=r"(q[13]),
+          "=r"(q[14]), "=r"(q[15])
+        : "r"(ta + ((uint32_t)(16 * y) << 16)) : "memory");
+  }
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {      // no use of a value moves above the wait
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[y][i]) :: "memory");
+  }
 }
 
-// 32 TMEM lanes x 16 columns: lane l gets its lane's columns.
-__device__ __forceinline__ void tmem_ld_x16(uint32_t ta, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(ta) : "memory");
-  asm volatile(
-      "tcgen05.wait::ld.sync.aligned;"
-      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-      :: "memory");
+// Four 8 x 8 matrices of 16-bit values, stored transposed: a lane holds row lane / 4, columns
+// 2 (lane % 4) and the next, of each; lane 8 i + j gives the address of column j of matrix i.
+__device__ __forceinline__ void stmatrix4_trans(uint8_t* d, const uint32_t (&v)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+               ::"r"(tc::smem_u32(d)), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+// 16-byte piece cc of head h's 64-byte row: eight heads' pieces cover all banks.
+__device__ __forceinline__ uint8_t* stage_at(uint8_t* stage, int h, int cc) {
+  return stage + h * 64 + ((cc ^ ((h >> 1) & 3)) << 4);
+}
+
+// A box of the output from shared memory to device memory, by one thread and asynchronously.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* tm, const void* src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n\t"
+               "cp.async.bulk.commit_group;"
+               ::"l"(tm), "r"(x), "r"(y), "r"(tc::smem_u32(src)) : "memory");
+}
+// This thread's stores have read shared memory.
+__device__ __forceinline__ void tma_store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 // The query heads of a token into shared memory (cp.async, by the producer warps).
@@ -449,7 +463,8 @@ __device__ __forceinline__ float rel_weight(float x, float top) {
 
 template <bool FP8>
 __global__ void __launch_bounds__(kLaunch, 1)
-    chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ ChunkTc p) {
+    chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_rows,
+                    const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ ChunkTc p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* sKV = base;                            // 8 x 16 KB
@@ -459,7 +474,8 @@ __global__ void __launch_bounds__(kLaunch, 1)
   float* s_M = s_red + 4 * kH;                    // running reference maximum, log2 units
   float* s_alpha = s_M + kH;
   float* s_sink2 = s_alpha + kH;
-  int* s_flag = reinterpret_cast<int*>(s_sink2 + kH);
+  float2* s_rot = reinterpret_cast<float2*>(s_sink2 + kH);   // the output's rotation: sine, cosine
+  int* s_flag = reinterpret_cast<int*>(s_rot + kMaxOutRopePairs);
   uint64_t* bar_s = reinterpret_cast<uint64_t*>(s_flag + 4);
   uint64_t* bar_pv = bar_s + 1;                   // [4]
   uint64_t* bar_full = bar_pv + 4;                // [4]: a pair of the tile is in place
@@ -755,8 +771,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
         // (lg[y]: rows r0 + 16 y, 8 further)
         uint32_t lg[2][16];
         auto logits = [&]() {
-#pragma unroll
-          for (int y = 0; y < 2; ++y) tmem_ld16(tS + lane_addr + ((uint32_t)(16 * y) << 16) + 32 * hf, lg[y]);
+          tmem_ld16x2(tS + lane_addr + 32 * hf, lg);
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
 #pragma unroll
@@ -800,6 +815,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
             for (int h = 0; h < 8; ++h) v[h] = fmaxf(v[h], __shfl_xor_sync(0xffffffffu, v[h], o));
           }
           if (tid == 0) s_flag[0] = 0;             // its last reads are behind a barrier
+          if (lane == 0) tma_store_wait_read();    // an item's first P^T comes after this and the barrier
           if (lane < 4) {
 #pragma unroll
             for (int g = 0; g < 4; ++g)
@@ -913,6 +929,10 @@ __global__ void __launch_bounds__(kLaunch, 1)
           s_alpha[tid] = den == 0.f ? 0.f : wr / den;
           if (p.lse) p.lse[(long long)I.tok * kH + tid] = den == 0.f ? -INFINITY : (top + log2f(den)) * kLn2;
         }
+      } else if (tid < kH + p.d_rope_out / 2 && p.nsplit == 1) {
+        float sn, cs;
+        rope_angle((double)I.t * p.inv_freq[tid - kH], &sn, &cs);
+        s_rot[tid - kH] = make_float2(sn, cs);
       }
       tc::named_bar(3, kST);
       if (p.nsplit > 1) {
@@ -929,49 +949,80 @@ __global__ void __launch_bounds__(kLaunch, 1)
           for (int h = 0; h < 32; ++h) dst[h * kD] = ok ? __uint_as_float(o[h]) : nan_f();
         }
       } else {
-        // 16 heads at a time, their factors in registers over the four dim blocks (a shared-memory
-        // read for each pair of heads and block cost 7 % of a selected chunk)
-        const int odd = lane & 1, d0 = row & ~1;
-#pragma unroll 1
-        for (int hh = 0; hh < 32; hh += 16) {
-          float w[16];
+        // A warp's 32 dims of 32 heads of each dim block become [head][dim] rows of 64 bytes in
+        // the warp's part of P^T, which the PVs have read by then (stmatrix transposes 8 x 8
+        // values at a time), and leave by TMA.  (Pairs exchanged by shuffles and stored in 4
+        // bytes queued behind the loads of the producers: a selected chunk 2 % slower, 5 % in bf16.)
+        uint8_t* stage = sP + warp * 2048;
+        float w[8];
 #pragma unroll
-          for (int h = 0; h < 16; h += 4) {
-            const float4 w4 = *reinterpret_cast<const float4*>(s_alpha + 32 * hf + hh + h);
-            w[h] = w4.x; w[h + 1] = w4.y; w[h + 2] = w4.z; w[h + 3] = w4.w;
-          }
+        for (int g = 0; g < 4; ++g) {
+          const float2 w2 = *reinterpret_cast<const float2*>(s_alpha + h0 + 8 * g);
+          w[2 * g] = w2.x;
+          w[2 * g + 1] = w2.y;
+        }
+        const int rope0 = kD - p.d_rope_out;
 #pragma unroll 1
-          for (int mb = 0; mb < 4; ++mb) {
-            if (hh == 0) ok = ok && tc::mbar_wait_hint(bar_pv + mb, (ns - 1) & 1, p.err, kHintNs);
-            tc::tc_fence_after();
-            uint32_t o[16];
-            tmem_ld_x16(tO + mb * kH + 32 * hf + hh + lane_addr, o);
-            // lanes 2i and 2i + 1 hold dims 2i and 2i + 1 of every head: the even lane takes both
-            // of head h, the odd one both of head h + 1, for 4-byte stores and the rotary pair
-            const int d = mb * 128 + d0;
-            const bool rot = d >= kD - p.d_rope_out;
-            float sn = 0.f, cs = 1.f;
-            if (rot) rope_angle((double)I.t * p.inv_freq[(d - (kD - p.d_rope_out)) >> 1], &sn, &cs);
-            __nv_bfloat16* dst = p.out + ((long long)I.tok * kH + 32 * hf + hh + odd) * kD + d;
+        for (int mb = 0; mb < 4; ++mb) {
+          ok = ok && tc::mbar_wait_hint(bar_pv + mb, (ns - 1) & 1, p.err, kHintNs);
+          tc::tc_fence_after();
+          uint32_t ob[2][16];
+          tmem_ld16x2(tO + mb * kH + 32 * hf + lane_addr, ob);
 #pragma unroll
-            for (int h = 0; h < 16; h += 2) {
-              const float a = w[h] == 0.f ? 0.f : __uint_as_float(o[h]) * w[h];
-              const float c = w[h + 1] == 0.f ? 0.f : __uint_as_float(o[h + 1]) * w[h + 1];
-              const float got = __shfl_xor_sync(0xffffffffu, odd ? a : c, 1);
-              float x0 = odd ? got : a, x1 = odd ? c : got;
-              if (rot) {
-                const float y0 = fmaf(x0, cs, x1 * sn), y1 = fmaf(x1, cs, -x0 * sn);
-                x0 = y0; x1 = y1;
+          for (int y = 0; y < 2; ++y) {
+            uint32_t(&o)[16] = ob[y];
+            const int d0 = mb * 128 + 32 * qd + 16 * y;   // this lane's dims: d0 + lane / 4, 8 further
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float f = w[2 * (i >> 2) + (i & 1)];
+              o[i] = __float_as_uint(f == 0.f ? 0.f : __uint_as_float(o[i]) * f);
+            }
+            if (d0 + 16 > rope0) {                        // the other dim of a pair: lane ^ 4
+              const int odd = (lane >> 2) & 1;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int u = d0 + 8 * e + (lane >> 2) - rope0;
+                const float2 r = u >= 0 ? s_rot[u >> 1] : make_float2(0.f, 1.f);
+                const float sn = odd ? -r.x : r.x;
+#pragma unroll
+                for (int i = 2 * e; i < 16; i += (i & 1) ? 3 : 1) {
+                  const float x = __uint_as_float(o[i]);
+                  const float z = __shfl_xor_sync(0xffffffffu, x, 4);
+                  if (u >= 0) o[i] = __float_as_uint(fmaf(x, r.y, z * sn));
+                }
               }
-              if (!ok) x0 = x1 = nan_f();
-              *reinterpret_cast<__nv_bfloat162*>(dst + h * kD) = __floats2bfloat162_rn(x0, x1);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {                 // packed in place: o[i] heads 2 i, 2 i + 1
+              const __nv_bfloat162 b2 =
+                  __floats2bfloat162_rn(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+              o[i] = *reinterpret_cast<const uint32_t*>(&b2);
             }
           }
+          // the stage is free: the last PV has read P^T, the store of the block before its rows
+          if (mb == 0) ok = ok && tc::mbar_wait_hint(bar_pv + 3, (ns - 1) & 1, p.err, kHintNs);
+          if (lane == 0) tma_store_wait_read();
+          __syncwarp();
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {                 // 16 heads x 16 dims
+              uint32_t v[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) v[i] = ok ? ob[y][4 * a + i] : 0x7fff7fffu;
+              const int h = 16 * a + 8 * (lane >> 4) + (lane & 7);
+              stmatrix4_trans(stage_at(stage, h, 2 * y + ((lane >> 3) & 1)), v);
+            }
+          }
+          tc::fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) tma_store_2d(&tm_out, stage, mb * 256 + qd * 64, I.tok * kH + 32 * hf);
         }
       }
       tc::tc_fence_before();
       tc::named_bar(3, kST);                       // s_red, s_alpha and s_M are free again
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
 
   tc::tc_fence_before();
@@ -1032,7 +1083,7 @@ __global__ void __launch_bounds__(128 * kMergeHeads) chunk_merge_kernel(const __
   *reinterpret_cast<uint2*>(p.out + ((long long)tok * kH + h) * kD + d) = v;
 }
 
-constexpr size_t kSmem = 1024 + 8 * kKVBlk + 8 * kQBlk + kRows * 128 + (4 * kH + 3 * kH) * 4 + 16 + 9 * 8 + 8 + 16 +
+constexpr size_t kSmem = 1024 + 8 * kKVBlk + 8 * kQBlk + kRows * 128 + (4 * kH + 3 * kH) * 4 + kMaxOutRopePairs * 8 + 16 + 9 * 8 + 8 + 16 +
                          (2 * kSeqCache + 1 + 2 * kSeqOrder + 1) * 4;
 static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 
@@ -1114,12 +1165,16 @@ csa_status launch_chunk_attn_tc(const ChunkArgs& a, const csa_kv_cache& kv, void
   if (kv.dtype == CSA_BF16 &&
       !make_tmap_2d_b16(&tm, kv.rows, kD, (uint64_t)kv.num_pages * kPageEntries, 64, kRows))
     return CSA_ERR_CUDA;
+  // the output as rows of one head, stored in boxes of 32 dims of 32 heads
+  CUtensorMap tm_out{};
+  if (p.nsplit == 1 && !make_tmap_2d_u8_swz(&tm_out, a.out, kD * 2, (uint64_t)a.N * kH, 64, 32, 64))
+    return CSA_ERR_CUDA;
   const int grid = (int)std::min<long long>(items, sm_count());
   // Several rounds of items of several sequences: longest first, so that no CTA meets a long
   // token last.  (One token of 44 tiles before 927 of 1 to 17: 431 us in the given order, 310 in
   // this; more sequences than kSeqOrder even out by themselves, and sorting them would take long.)
   p.order = p.items > grid && a.b > 1 && a.b <= kSeqOrder;
-  if (csa_launch(kern, dim3(grid), dim3(kLaunch), kSmem, st, false, tm, p) != cudaSuccess) return CSA_ERR_CUDA;
+  if (csa_launch(kern, dim3(grid), dim3(kLaunch), kSmem, st, false, tm, tm_out, p) != cudaSuccess) return CSA_ERR_CUDA;
   if (p.nsplit > 1 &&
       csa_launch(chunk_merge_kernel, dim3(a.N, kH / kMergeHeads), dim3(128 * kMergeHeads), 0, st, true, p) != cudaSuccess)
     return CSA_ERR_CUDA;
