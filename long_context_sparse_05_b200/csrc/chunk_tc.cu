@@ -19,7 +19,9 @@
 // stored, they travel under this tile's softmax and PV, and each 128-dim pair is stored the
 // moment the PV has read its predecessor; its S^T MMAs start on it.  FP8 rows become bf16 on
 // the way to shared memory (code times a power of two: exact).  A whole tile of neighbouring
-// bf16 rows needs no registers: TMA puts each pair in place as soon as that is free.  Chosen
+// bf16 rows, of a page or of new_win, needs no registers: TMA puts each pair in place as soon
+// as that is free (windows through registers: a selected FP8 chunk 668 us instead of 618).
+// Chosen
 // rows go through registers, since row gathers by TMA (one row of 128 bytes after another)
 // moved 9 to 25 bytes a cycle and SM against 55 to 80.  A dense bf16 tile takes ~6,100 cycles,
 // one of FP8 ~7,500.  Measured and not taken: loads and softmax in the same warps (10,400
@@ -27,7 +29,7 @@
 // tiles of 64 rows in turn (M = 64 halves the MMA's rate: a dense chunk 27 % slower).
 //
 // The softmax keeps the maximum lazily (raised only when a tile exceeds it by 2^8, which
-// rescales O^T in TMEM) and each thread's sums of its 32 heads in registers over the tiles of
+// rescales O^T in TMEM) and each thread's sums of its eight heads in registers over the tiles of
 // an item: the reduction over the rows runs once per item, so an ordinary tile needs one
 // barrier (the OR of "some logit exceeds the maximum") before its probabilities.
 //
@@ -464,6 +466,7 @@ __device__ __forceinline__ float rel_weight(float x, float top) {
 template <bool FP8>
 __global__ void __launch_bounds__(kLaunch, 1)
     chunk_tc_kernel(const __grid_constant__ CUtensorMap tm_rows,
+                    const __grid_constant__ CUtensorMap tm_new,
                     const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ ChunkTc p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -638,8 +641,14 @@ __global__ void __launch_bounds__(kLaunch, 1)
       new_q = S.n != item;
       item = S.n;
       have = __ballot_sync(0xffffffffu, code >= 0);
-      // 128 consecutive rows of one page that all exist come by TMA, straight into the tile
-      whole = !FP8 && !window && !p.idx && (S.tile + 1) * kRows <= S.it.nsel && have == 0xffffffffu;
+      // 128 consecutive bf16 rows that all exist, of one page or of new_win, come by TMA,
+      // straight into the tile
+      if (window) {
+        const int u = S.it.w0 + (S.tile - S.it.ne) * kRows;
+        whole = u >= S.it.p0 && u + kRows - 1 <= S.it.t;
+      } else {
+        whole = !FP8 && !p.idx && (S.tile + 1) * kRows <= S.it.nsel && have == 0xffffffffu;
+      }
       row_numbers(c4, code, lane);
       if (FP8 && !window) {
         if constexpr (FP8) load_fp8(st, sc, c4, p, code, lane);
@@ -676,18 +685,20 @@ __global__ void __launch_bounds__(kLaunch, 1)
         if (lane == 0) s_valid16[w] = (uint16_t)have;
         if (wait_q) tc::cp_async_wait_all();
       };
-      if (!FP8 && whole) {
+      if (whole) {
+        const CUtensorMap* tm = window ? &tm_new : &tm_rows;
+        const int first = window ? code & (kNewTag - 1) : code;   // (lane 0 of warp 0)
 #pragma unroll
         for (int mb = 0; mb < 4; ++mb) {
           wait_pv(mb);
           if (mb == 0) ready();
-          if (w == 0) {                            // lane 0's row is the tile's first
+          if (w == 0) {
             tc::fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
               tc::mbar_arrive_expect_tx(bar_full + mb, 2 * kKVBlk);
-              tc::tma_load_2d(sKV + 2 * mb * kKVBlk, &tm_rows, 128 * mb, code, bar_full + mb);
-              tc::tma_load_2d(sKV + (2 * mb + 1) * kKVBlk, &tm_rows, 128 * mb + 64, code, bar_full + mb);
+              tc::tma_load_2d(sKV + 2 * mb * kKVBlk, tm, 128 * mb, first, bar_full + mb);
+              tc::tma_load_2d(sKV + (2 * mb + 1) * kKVBlk, tm, 128 * mb + 64, first, bar_full + mb);
             }
           } else {
             warp_arrive(bar_full + mb, lane);
@@ -1165,6 +1176,10 @@ csa_status launch_chunk_attn_tc(const ChunkArgs& a, const csa_kv_cache& kv, void
   if (kv.dtype == CSA_BF16 &&
       !make_tmap_2d_b16(&tm, kv.rows, kD, (uint64_t)kv.num_pages * kPageEntries, 64, kRows))
     return CSA_ERR_CUDA;
+  CUtensorMap tm_new{};
+  if (a.n_w >= kRows && a.N >= kRows &&            // (a whole tile of new rows needs both)
+      !make_tmap_2d_b16(&tm_new, a.new_win, kD, (uint64_t)a.N, 64, kRows))
+    return CSA_ERR_CUDA;
   // the output as rows of one head, stored in boxes of 32 dims of 32 heads
   CUtensorMap tm_out{};
   if (p.nsplit == 1 && !make_tmap_2d_u8_swz(&tm_out, a.out, kD * 2, (uint64_t)a.N * kH, 64, 32, 64))
@@ -1174,7 +1189,7 @@ csa_status launch_chunk_attn_tc(const ChunkArgs& a, const csa_kv_cache& kv, void
   // token last.  (One token of 44 tiles before 927 of 1 to 17: 431 us in the given order, 310 in
   // this; more sequences than kSeqOrder even out by themselves, and sorting them would take long.)
   p.order = p.items > grid && a.b > 1 && a.b <= kSeqOrder;
-  if (csa_launch(kern, dim3(grid), dim3(kLaunch), kSmem, st, false, tm, tm_out, p) != cudaSuccess) return CSA_ERR_CUDA;
+  if (csa_launch(kern, dim3(grid), dim3(kLaunch), kSmem, st, false, tm, tm_new, tm_out, p) != cudaSuccess) return CSA_ERR_CUDA;
   if (p.nsplit > 1 &&
       csa_launch(chunk_merge_kernel, dim3(a.N, kH / kMergeHeads), dim3(128 * kMergeHeads), 0, st, true, p) != cudaSuccess)
     return CSA_ERR_CUDA;

@@ -537,6 +537,21 @@ def test_chunk_attn_a_head_of_infinities(cfg):
     c.check(tokens=5)
 
 
+@pytest.mark.parametrize("fmt,d_hi", [(L.CSA_BF16, 0), (L.CSA_FP8_E4M3, 64)])
+@pytest.mark.parametrize("cfg", [
+    dict(lens=[310, 140], ctx=[700, 0], n_w=300, k=64),              # whole tiles of new rows, then a part
+    dict(lens=[450], ctx=[77], n_w=256, k=0),                        # part of the first from the rings
+    dict(lens=[128], ctx=[0], n_w=128, k=16, pad=0),                 # one token with a whole tile
+    dict(lens=[127], ctx=[1], n_w=128, k=16, pad=0),                 # fewer rows than a tile
+    dict(lens=[60, 200, 60], ctx=[0, 5, 900], n_w=129, k=64),
+    dict(lens=[400], ctx=[0], n_w=128, k=64, counts=0),              # the window alone
+])
+def test_chunk_attn_windows_of_new_rows(fmt, d_hi, cfg):
+    c = dict(TC, m=4, seed=91, fmt=fmt, d_hi=d_hi, nan_rest=True, d_rope_out=64)
+    c.update(cfg)
+    Case(**c).run().check(tokens=12)
+
+
 @pytest.mark.parametrize("b", [33, 1100])
 def test_chunk_attn_many_sequences(b):
     """More sequences than one step of the search, and than shared memory holds."""
