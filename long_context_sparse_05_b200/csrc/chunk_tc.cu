@@ -78,6 +78,8 @@ static_assert(kRegsSoftmax <= kRegsLaunch && kRegsProd >= kRegsLaunch && kRegsMm
 constexpr uint32_t kHintNs = 64;
 constexpr int kSeqCache = 1024;       // sequences whose boundaries are kept in shared memory
 constexpr int kSeqOrder = 64;         // sequences that are taken in order of length
+constexpr int kItemList = 1024;       // items of a CTA that are chosen by load
+constexpr int kMaxCtas = 160;         // ... of CTAs whose loads a warp keeps in registers
 constexpr int kMaxSplit = 32;
 constexpr int kNewTag = 1 << 30;      // window rows: new_win's row + kNewTag, or the rings' row
 
@@ -101,27 +103,34 @@ struct Item {
 };
 
 // The sequences as the CTAs walk them: boundaries and first positions (in shared memory where
-// they fit), and, where the sequences are taken longest first, their order and the boundaries
-// in that order.
+// they fit), and, where the sequences are taken longest first, their order, the boundaries in
+// that order and this CTA's items.
 struct Seqs {
-  const int32_t* s;        // shared memory: cu [kSeqCache + 1], pos0 [kSeqCache], cum, ord
-  bool cached, ordered;
-  __device__ __forceinline__ const int32_t* cu(const ChunkTc& p) const { return cached ? s : p.cu_q; }
+  // shared memory: cu [kSeqCache + 1], pos0 [kSeqCache], cum [kSeqOrder + 1], ord [kSeqOrder],
+  // whether cum and ord hold, the list's length (-1: none), the list
+  const int32_t* s;
+  static constexpr int kPos0 = kSeqCache + 1, kCum = kPos0 + kSeqCache, kOrd = kCum + kSeqOrder + 1;
+  static constexpr int kOrdered = kOrd + kSeqOrder, kListed = kOrdered + 1, kList = kListed + 1;
+  static constexpr int kWords = kList + kItemList;
+  __device__ __forceinline__ bool ordered() const { return s[kOrdered] != 0; }
+  __device__ __forceinline__ const int32_t* cu(const ChunkTc& p) const {
+    return p.b <= kSeqCache ? s : p.cu_q;
+  }
   __device__ __forceinline__ const int32_t* pos0(const ChunkTc& p) const {
-    return cached ? s + kSeqCache + 1 : p.pos0;
+    return p.b <= kSeqCache ? s + kPos0 : p.pos0;
   }
   __device__ __forceinline__ const int32_t* cum(const ChunkTc& p) const {
-    return ordered ? s + 2 * kSeqCache + 1 : cu(p);
+    return ordered() ? s + kCum : cu(p);
   }
-  __device__ __forceinline__ int seq(int j) const {
-    return ordered ? s[2 * kSeqCache + 1 + kSeqOrder + 1 + j] : j;
-  }
+  __device__ __forceinline__ int seq(int j) const { return ordered() ? s[kOrd + j] : j; }
 };
 
-// The n-th item of this CTA.  In order of length, every other round runs the other way, so that
-// the CTA with the longest items of one round has the shortest of the next.
+// The n-th item of this CTA.  In order of length without a list, every other round runs the
+// other way, so that the CTA with the longest items of one round has the shortest of the next.
 __device__ __forceinline__ int item_at(const Seqs& q, int n) {
-  const int x = q.ordered && (n & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+  const int listed = q.s[Seqs::kListed];
+  if (listed >= 0) return n < listed ? q.s[Seqs::kList + n] : INT_MAX;
+  const int x = q.ordered() && (n & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
   return n * gridDim.x + x;
 }
 
@@ -156,6 +165,115 @@ __device__ __forceinline__ Item get_item(const ChunkTc& p, const Seqs& q, int it
   I.tb = split * tiles / p.nsplit;
   I.te = (split + 1) * tiles / p.nsplit;
   return I;
+}
+
+// This CTA's items, written to `list`: each item, longest sequences first, goes to the CTA
+// with the least load so far (whole warp; every CTA finds the same shares).  Neighbouring
+// sequences whose items cost about the same are dealt as one group: the least level that
+// holds the group's items gives each CTA's number of them, and they are dealt in rounds, so
+// that a sequence's early and late tokens spread.  Loads in half tiles; an item costs two
+// tiles beside its own (queries, first tile's latency, output).  -1: some CTA's list is full
+// (or the shares do not add up): not to be used.
+// One token of 44 tiles, 261 of 17 and 666 of 1 to 3: 274 us; dealt by turns 310.
+template <class Cost>
+__device__ __forceinline__ int share_items(const ChunkTc& p, const int32_t* cum, int32_t* list, int lane,
+                                           Cost cost_of) {
+  constexpr int Q = kMaxCtas / 32;
+  int load[Q], total[Q];                           // of CTA lane + 32 q
+#pragma unroll
+  for (int q = 0; q < Q; ++q) load[q] = total[q] = 0;
+  const int grid = gridDim.x, me = blockIdx.x;
+  auto valid = [&](int q) { return lane + 32 * q < grid; };
+  int got = 0;
+  bool dealt = true;
+  for (int j = 0; j < p.b;) {
+    const int first = cum[j] * p.nsplit;           // the group: sequences j .. j2 - 1
+    const int c0 = cost_of(j);
+    float work = 0.f;
+    int j2 = j;
+    for (; j2 < p.b; ++j2) {
+      const int c = cost_of(j2);
+      if (4 * c < 3 * c0) break;
+      work += (float)(cum[j2 + 1] - cum[j2]) * c;
+    }
+    const int n = (cum[j2] - cum[j]) * p.nsplit;
+    j = j2;
+    if (n <= 0) continue;
+    const int c = max(4, (int)(work * p.nsplit / n));
+    const float rc = 1.f / c;
+    // items of this group that a CTA takes below level L
+    auto below = [&](int q, int L) {
+      return valid(q) && load[q] < L ? (int)((L - 1 - load[q]) * rc) + 1 : 0;
+    };
+    auto held = [&](int L) {
+      int k = 0;
+#pragma unroll
+      for (int q = 0; q < Q; ++q) k += below(q, L);
+      return __reduce_add_sync(0xffffffffu, k);
+    };
+    long long sum = 0;
+    int lo = INT_MAX;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      sum += load[q];
+      if (valid(q)) lo = min(lo, load[q]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    lo = __reduce_min_sync(0xffffffffu, lo);       // holds none
+    int hi = (int)(((long long)n * c + sum) / grid) + c + 2;   // holds them all, rounding or not
+    while (hi - lo > 1) {
+      const int mid = lo + (hi - lo) / 2;
+      if (held(mid) < n) lo = mid; else hi = mid;
+    }
+    int extra = n - held(lo);                      // of those whose next item lies at the level
+    int k[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      k[q] = below(q, lo);
+      const bool more = below(q, hi) > k[q];
+      const unsigned b = __ballot_sync(0xffffffffu, more);
+      k[q] += more && __popc(b & ((1u << lane) - 1)) < extra ? 1 : 0;
+      extra -= __popc(b);                          // (negative: none left)
+      load[q] += k[q] * c;
+      total[q] += k[q];
+    }
+    // rounds: all CTAs at first, then those that take more than r items of the group, in order
+    int least = INT_MAX;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      if (valid(q)) least = min(least, k[q]);
+    }
+    least = __reduce_min_sync(0xffffffffu, least);
+    for (int r = lane; r < min(least, kItemList - got); r += 32) list[got + r] = first + r * grid + me;
+    got = min(got + least, kItemList);
+    int at = first + least * grid;
+    for (int r = least;; ++r) {
+      int all = 0, before = 0;
+      bool mine = false;
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const unsigned b = __ballot_sync(0xffffffffu, k[q] > r);
+        all += __popc(b);
+        if (q < me / 32) before += __popc(b);
+        if (q == me / 32) {
+          before += __popc(b & ((1u << (me % 32)) - 1));
+          mine = (b >> (me % 32)) & 1;
+        }
+      }
+      if (!all) break;
+      if (mine && got < kItemList) {
+        if (lane == 0) list[got] = at + before;
+        ++got;
+      }
+      at += all;
+    }
+    dealt = dealt && at == first + n;
+  }
+  int most = 0;
+#pragma unroll
+  for (int q = 0; q < Q; ++q) most = max(most, total[q]);
+  return __reduce_max_sync(0xffffffffu, most) > kItemList || !dealt ? -1 : got;
 }
 
 // The tiles of a CTA's items, one after another (empty items skipped).
@@ -485,19 +603,19 @@ __global__ void __launch_bounds__(kLaunch, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bar_full + 4);
   uint32_t* s_valid = tmem_holder + 2;            // [4] the tile's rows that exist, a bit each
   uint16_t* s_valid16 = reinterpret_cast<uint16_t*>(s_valid);   // ... as the producers write them
-  int32_t* s_cu = reinterpret_cast<int32_t*>(s_valid + 4);   // [kSeqCache + 1]
-  int32_t* s_pos0 = s_cu + kSeqCache + 1;         // [kSeqCache]
-  int32_t* s_cum = s_pos0 + kSeqCache;            // [kSeqOrder + 1]
-  int32_t* s_ord = s_cum + kSeqOrder + 1;         // [kSeqOrder]
+  int32_t* s_cu = reinterpret_cast<int32_t*>(s_valid + 4);   // [Seqs::kWords]
+  const Seqs seqs{s_cu};
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
-  const bool cached = p.b <= kSeqCache;
-  if (cached) {
+  if (p.b <= kSeqCache) {
     for (int i = tid; i <= p.b; i += kLaunch) s_cu[i] = p.cu_q[i];
-    for (int i = tid; i < p.b; i += kLaunch) s_pos0[i] = p.pos0[i];
+    for (int i = tid; i < p.b; i += kLaunch) s_cu[Seqs::kPos0 + i] = p.pos0[i];
   }
-  Seqs seqs{s_cu, cached, false};
+  if (tid == 0) {
+    s_cu[Seqs::kOrdered] = 0;
+    s_cu[Seqs::kListed] = -1;
+  }
   if (tid < kH) s_sink2[tid] = p.sink[tid] * kLog2e;
   if (tid == 0) {
     tc::mbar_init(bar_s, 1);
@@ -511,6 +629,8 @@ __global__ void __launch_bounds__(kLaunch, 1)
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   if (p.order && s_cu[p.b] <= p.N) {               // (uniform; b fits the cached part)
+    const int32_t* s_pos0 = s_cu + Seqs::kPos0;
+    int32_t *s_cum = s_cu + Seqs::kCum, *s_ord = s_cu + Seqs::kOrd;
     // rank of a sequence by the entries its last token sees, longest first
     const int s = tid;
     if (s < p.b) {
@@ -533,7 +653,22 @@ __global__ void __launch_bounds__(kLaunch, 1)
       s_cum[tid] = c;
     }
     __syncthreads();
-    seqs.ordered = true;
+    if (warp == 0) {
+      auto cost = [&](int j) {                     // half tiles, the mean of the first and the last token
+        const int x = s_ord[j], t0 = s_pos0[x], t1 = t0 + (s_cu[x + 1] - s_cu[x]) - 1;
+        auto tiles = [&](int t) {
+          const int e = min(max(0, (t + 1) / p.m), p.idx ? p.k : p.kv.max_pages * kPageEntries);
+          return (e + kRows - 1) / kRows + (min(max(0, t + 1), p.n_w) + kRows - 1) / kRows;
+        };
+        return (tiles(t0) + tiles(t1)) / p.nsplit + 4;
+      };
+      const int got = share_items(p, s_cum, s_cu + Seqs::kList, lane, cost);
+      if (lane == 0) {
+        s_cu[Seqs::kListed] = got;
+        s_cu[Seqs::kOrdered] = 1;
+      }
+    }
+    __syncthreads();
   }
   const uint32_t tS = tmem, tO = tmem + 64;       // columns [0, 64) S^T; [64, 320) O^T
 
@@ -1095,7 +1230,7 @@ __global__ void __launch_bounds__(128 * kMergeHeads) chunk_merge_kernel(const __
 }
 
 constexpr size_t kSmem = 1024 + 8 * kKVBlk + 8 * kQBlk + kRows * 128 + (4 * kH + 3 * kH) * 4 + kMaxOutRopePairs * 8 + 16 + 9 * 8 + 8 + 16 +
-                         (2 * kSeqCache + 1 + 2 * kSeqOrder + 1) * 4;
+                         Seqs::kWords * 4;
 static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 
 int sm_count() {
@@ -1185,10 +1320,10 @@ csa_status launch_chunk_attn_tc(const ChunkArgs& a, const csa_kv_cache& kv, void
   if (p.nsplit == 1 && !make_tmap_2d_u8_swz(&tm_out, a.out, kD * 2, (uint64_t)a.N * kH, 64, 32, 64))
     return CSA_ERR_CUDA;
   const int grid = (int)std::min<long long>(items, sm_count());
-  // Several rounds of items of several sequences: longest first, so that no CTA meets a long
-  // token last.  (One token of 44 tiles before 927 of 1 to 17: 431 us in the given order, 310 in
-  // this; more sequences than kSeqOrder even out by themselves, and sorting them would take long.)
-  p.order = p.items > grid && a.b > 1 && a.b <= kSeqOrder;
+  // Several rounds of items of several sequences: longest first, each to the CTA with the least
+  // load.  (One token of 44 tiles before 927 of 1 to 17: 434 us in the given order, 274 so; more
+  // sequences than kSeqOrder even out by themselves, and sorting them would take long.)
+  p.order = p.items > grid && a.b > 1 && a.b <= kSeqOrder && grid <= kMaxCtas;
   if (csa_launch(kern, dim3(grid), dim3(kLaunch), kSmem, st, false, tm, tm_new, tm_out, p) != cudaSuccess) return CSA_ERR_CUDA;
   if (p.nsplit > 1 &&
       csa_launch(chunk_merge_kernel, dim3(a.N, kH / kMergeHeads), dim3(128 * kMergeHeads), 0, st, true, p) != cudaSuccess)

@@ -552,6 +552,61 @@ def test_chunk_attn_windows_of_new_rows(fmt, d_hi, cfg):
     Case(**c).run().check(tokens=12)
 
 
+def _one_by_one(c, n_least):
+    """Each sequence of a case by itself, in a call of at least n_least rows (so that neither is
+    split): the same output, bit for bit."""
+    out, lse = c.out.clone(), c.lse.clone()
+    bt = i32(c.bt.tolist())
+    for s in range(c.b):
+        lo, hi = c.cu[s], c.cu[s + 1]
+        n = max(hi - lo, n_least)
+        kv = L.kv_cache(c.fmt, c.d, c.d_hi, *c.kv._tensors[:3], bt[s:s + 1].contiguous())
+
+        def part(x):
+            y = torch.zeros((n,) + tuple(x.shape[1:]), dtype=x.dtype, device="cuda")
+            y[:hi - lo] = x[lo:hi]
+            return y
+
+        o = torch.empty((n,) + tuple(out.shape[1:]), dtype=out.dtype, device="cuda")
+        e = torch.empty((n, c.H), device="cuda")
+        assert L.csa_chunk_attn_workspace_size(c.p, kv, 1, n, c.L_max) == 0
+        L.csa_chunk_attn(c.p, kv, part(c.q), i32([0, hi - lo]), i32([c.ctx[s]]),
+                         part(c.idx) if c.k else None, part(c.count) if c.k else None,
+                         c.win[s:s + 1].contiguous(), part(c.new_win), c.sink, 1, n, c.L_max, o, e, None)
+        torch.cuda.synchronize()
+        assert torch.equal(out[lo:hi], o[:hi - lo]) and torch.equal(lse[lo:hi], e[:hi - lo]), s
+
+
+@pytest.mark.parametrize("fmt,d_hi", [(L.CSA_BF16, 0), (L.CSA_FP8_E4M3, 64)])
+@pytest.mark.parametrize("lens,ctx,k", [
+    ([1, 37, 300, 29, 61], [70001, 0, 131, 3000, 25500], 0),         # one long token, many short
+    ([0, 200, 0, 3, 160, 0], [9, 5000, 0, 40, 0, 77], 0),            # sequences without tokens
+    ([5] * 63 + [9], list(range(0, 64 * 300, 300)), 0),              # as many as are ordered
+    ([7] * 65, list(range(0, 65 * 300, 300)), 0),                    # one more
+    ([300, 200], [4000, 0], 64),
+    ([149, 148, 1], [0, 0, 0], 0),                                   # equal ones
+])
+def test_chunk_attn_shared_out(fmt, d_hi, lens, ctx, k):
+    c = Case(lens, ctx, m=4, k=k, seed=101, fmt=fmt, d_hi=d_hi, d_rope_out=64, **TC).run()
+    assert c.N >= 296 and torch.all(c.out[c.cu[-1]:] == 7.0)
+    _one_by_one(c, 296)
+
+
+def test_chunk_attn_shared_out_long_lists():
+    """147 tokens of 3,200 tiles (nearly all on pages outside the pool) and 1,300 of one: a CTA
+    would take more items than its list holds."""
+    m, e = 4096, 3200 * 128
+    t = e * m
+    c = Case([147, 1300], [0, 0], m=4, k=0, seed=111, fmt=L.CSA_BF16, **TC)
+    bt = torch.full((2, e // PE), -1, dtype=torch.int32, device="cuda")
+    bt[0, 0], bt[0, -1], bt[1, 0] = 1, 0, 1
+    c.bt, c.kv = bt.cpu().numpy(), L.kv_cache(c.fmt, c.d, c.d_hi, *c.kv._tensors[:3], bt)
+    c.p.m, c.ctx, c.L_max = m, [t, 0], t + 147
+    c.run()
+    _one_by_one(c, 296)
+    assert torch.all(torch.isfinite(c.out[:c.cu[-1]].float()))
+
+
 @pytest.mark.parametrize("b", [33, 1100])
 def test_chunk_attn_many_sequences(b):
     """More sequences than one step of the search, and than shared memory holds."""
