@@ -15,8 +15,11 @@
  *                     selected entries plus a raw sliding window; dense over all
  *                     visible entries when no index list is given (HCA).
  *
- * plus csa_quantize (the index-path quantiser on its own) and the fused
- * drivers csa_decode and csa_prefill that chain the stages on one stream.
+ * plus csa_quantize (the index-path quantiser on its own), the fused drivers
+ * csa_decode and csa_prefill that chain the stages on one stream, and the calls
+ * that serve ragged chunks of new tokens over a paged cache, plain or quantised
+ * (csa_qk_norm_rope, csa_cache_write, csa_chunk_attn, csa_window_append,
+ * csa_cache_read; last section).
  *
  * Conventions for every call:
  *  - Pointers named as tensors are DEVICE pointers, allocated and owned by the
@@ -38,7 +41,8 @@
  * Storage types (csa_dtype):
  *  - CSA_F32, CSA_BF16: plain element arrays.
  *  - CSA_FP8_E4M3: one byte per element (OCP E4M3FN), plus one float32 scale
- *    per row: value = decode(code) * scale, scale = amax(row) / 448.
+ *    per row: value = decode(code) * scale, scale = amax(row) / 448.  (A
+ *    csa_kv_cache of this type has scales of its own, described there.)
  *  - CSA_NVFP4: two E2M1 codes per byte (element 2j in bits 0-3, 2j+1 in bits
  *    4-7), plus one UE4M3 scale byte per 16 consecutive elements:
  *    value = decode(code) * decode(scale), scale = e4m3(amax(block) / 6).
@@ -728,8 +732,8 @@ csa_status csa_qk_norm_rope(const csa_norm_rope_params* p, const void* q, int64_
  * formulas (p as there; p->dtype is the type of q, win, new_win and out), with
  *   token i of sequence s   row cu_q[s] + i of q, at position t = pos0[s] + i
  *   its entries             kv's entries idx[row][j], j < count[row] <= k; with idx NULL (and
- *                           then p->k = 0) every entry below E(t) = floor((t+1)/m).  kv->c = p->d; kv->dtype is
- *                           p->dtype, or CSA_FP8_E4M3
+ *                           then p->k = 0) every entry below E(t) = floor((t+1)/m).
+ *                           kv->c = p->d; kv->dtype is p->dtype, or CSA_FP8_E4M3
  *   its window              tokens max(0, t-n_w+1) .. t: the row of token u is new_win's row
  *                           cu_q[s] + u - pos0[s] from pos0[s] on, and slot u % n_w of win[s]
  *                           before (the rings as csa_decode_paged and csa_window_append keep

@@ -23,10 +23,12 @@
 // as that is free (windows through registers: a selected FP8 chunk 668 us instead of 618).
 // Chosen
 // rows go through registers, since row gathers by TMA (one row of 128 bytes after another)
-// moved 9 to 25 bytes a cycle and SM against 55 to 80.  A dense bf16 tile takes ~6,100 cycles,
-// one of FP8 ~7,500.  Measured and not taken: loads and softmax in the same warps (10,400
-// cycles: the softmax's shuffles and shared-memory accesses queue behind the loads), and two
-// tiles of 64 rows in turn (M = 64 halves the MMA's rate: a dense chunk 27 % slower).
+// moved 9 to 25 bytes a cycle and SM against 55 to 80.  A dense bf16 tile takes 2.75 us (5,400
+// cycles), one of chosen bf16 rows 3.7, of FP8 rows 3.9, and a token 8 to 9 us beside its tiles
+// (queries, the first tile's maxima, the last PV, the output).  Measured and not taken: loads
+// and softmax in the same warps (10,400 cycles: the softmax's shuffles and shared-memory
+// accesses queue behind the loads), and two tiles of 64 rows in turn (M = 64 halves the MMA's
+// rate: a dense chunk 27 % slower).
 //
 // The softmax keeps the maximum lazily (raised only when a tile exceeds it by 2^8, which
 // rescales O^T in TMEM) and each thread's sums of its eight heads in registers over the tiles of
