@@ -607,6 +607,38 @@ def test_chunk_attn_shared_out_long_lists():
     assert torch.all(torch.isfinite(c.out[:c.cu[-1]].float()))
 
 
+def test_captured_shares_follow_the_lengths():
+    """A replay shares its items out by the lengths it then finds."""
+    c = Case([200, 130], [2900, 50], m=4, k=0, seed=121, fmt=L.CSA_BF16, **TC)
+    cu, pos0 = i32([0, 200, 330]), i32([2900, 50])
+
+    def call():
+        L.csa_chunk_attn(c.p, c.kv, c.q, cu, pos0, None, None, c.win, c.new_win, c.sink, 2, c.N,
+                         c.L_max, c.out, c.lse, c.ws)
+
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for lens, ctx in (([200, 130], [2900, 50]), ([30, 300], [2900, 0]), ([0, 310], [7, 20])):
+        cu.copy_(i32(starts(lens)))
+        pos0.copy_(i32(ctx))
+        c.out.fill_(3.0)
+        g.replay()
+        torch.cuda.synchronize()
+        got, glse = c.out.clone(), c.lse.clone()
+        c.out.fill_(3.0)
+        call()
+        torch.cuda.synchronize()
+        assert L.csa_device_error() == 0
+        assert torch.equal(got, c.out) and torch.equal(glse, c.lse)
+        c.lens, c.ctx, c.cu = lens, ctx, starts(lens)
+        assert torch.all(c.out[c.cu[-1]:] == 3.0)
+        c.out[c.cu[-1]:], c.lse[c.cu[-1]:] = 7.0, 7.0
+        c.check(tokens=4)
+
+
 @pytest.mark.parametrize("b", [33, 1100])
 def test_chunk_attn_many_sequences(b):
     """More sequences than one step of the search, and than shared memory holds."""
