@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(32 * kLcWarps, 5) write_fp8_kernel(csa_kv_cach
   const int lane = threadIdx.x & 31;
   const int r0 = (blockIdx.x * kLcWarps + (threadIdx.x >> 5)) * R;
   if (r0 >= a.rows) return;
+  const int live = min(a.rows, a.cu[a.b]);   // x may end there: `rows` is only a bound
   const int nc = kv.c - kv.d_hi, S = kv_scale_stride(kv.c, kv.d_hi);
   uint8_t* codes = static_cast<uint8_t*>(kv.rows);
   __nv_bfloat16* hi = static_cast<__nv_bfloat16*>(kv.hi);
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(32 * kLcWarps, 5) write_fp8_kernel(csa_kv_cach
     Run16<T> x[R];
 #pragma unroll
     for (int i = 0; i < R; ++i)   // the row's values do not depend on where it goes
-      if (r0 + i < a.rows && ch < kv.c)
+      if (r0 + i < live && ch < kv.c)
         x[i].load(reinterpret_cast<const T*>(a.x) + (long long)(r0 + i) * a.x_stride + ch);
     if (c0 == 0) dest_rows(at, kv, a, r0, lane);
 #pragma unroll
