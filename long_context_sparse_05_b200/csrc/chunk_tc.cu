@@ -85,6 +85,9 @@ constexpr int kMaxCtas = 160;         // ... of CTAs whose loads a warp keeps in
 constexpr int kMaxSplit = 32;
 constexpr int kNewTag = 1 << 30;      // window rows: new_win's row + kNewTag, or the rings' row
 
+// Tiles of n >= 0 rows (n up to 2^31 - 1).
+__host__ __device__ __forceinline__ int tiles_of(int n) { return (int)(((unsigned)n + (kRows - 1)) / kRows); }
+
 struct ChunkTc {
   const __nv_bfloat16 *q, *win, *new_win;
   const int32_t *cu_q, *pos0, *idx, *count;
@@ -162,8 +165,8 @@ __device__ __forceinline__ Item get_item(const ChunkTc& p, const Seqs& q, int it
     nwin = I.t - I.w0 + 1;
   }
   I.nsel = max(0, ns);
-  I.ne = (I.nsel + kRows - 1) / kRows;
-  const int tiles = I.ne + (nwin + kRows - 1) / kRows;
+  I.ne = tiles_of(I.nsel);
+  const int tiles = I.ne + tiles_of(nwin);
   I.tb = split * tiles / p.nsplit;
   I.te = (split + 1) * tiles / p.nsplit;
   return I;
@@ -311,8 +314,11 @@ __device__ __forceinline__ void row_entry(RowRef& r, const Stream& s, const Chun
     if (pos < I.nsel) r.e = p.idx ? p.idx[(long long)I.tok * p.k + pos] : pos;
   } else {
     r.window = true;
-    const int u = I.w0 + (s.tile - I.ne) * kRows + row;
-    if (u <= I.t) r.e = u >= I.p0 ? kNewTag + I.i0 + (u - I.p0) : I.seq * p.n_w + u % p.n_w;
+    const int x = (s.tile - I.ne) * kRows + row;
+    if (x <= I.t - I.w0) {                         // (past t, w0 + x may pass 2^31)
+      const int u = I.w0 + x;
+      r.e = u >= I.p0 ? kNewTag + I.i0 + (u - I.p0) : I.seq * p.n_w + u % p.n_w;
+    }
   }
 }
 __device__ __forceinline__ void row_page(RowRef& r, int seq, const ChunkTc& p) {
@@ -660,7 +666,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
         const int x = s_ord[j], t0 = s_pos0[x], t1 = t0 + (s_cu[x + 1] - s_cu[x]) - 1;
         auto tiles = [&](int t) {
           const int e = min(max(0, (t + 1) / p.m), p.idx ? p.k : p.kv.max_pages * kPageEntries);
-          return (e + kRows - 1) / kRows + (min(max(0, t + 1), p.n_w) + kRows - 1) / kRows;
+          return tiles_of(e) + tiles_of(min(max(0, t + 1), p.n_w));
         };
         return (tiles(t0) + tiles(t1)) / p.nsplit + 4;
       };
@@ -782,9 +788,9 @@ __global__ void __launch_bounds__(kLaunch, 1)
       // straight into the tile
       if (window) {
         const int u = S.it.w0 + (S.tile - S.it.ne) * kRows;
-        whole = u >= S.it.p0 && u + kRows - 1 <= S.it.t;
+        whole = u >= S.it.p0 && u <= S.it.t - (kRows - 1);
       } else {
-        whole = !FP8 && !p.idx && (S.tile + 1) * kRows <= S.it.nsel && have == 0xffffffffu;
+        whole = !FP8 && !p.idx && S.tile < S.it.nsel / kRows && have == 0xffffffffu;
       }
       row_numbers(c4, code, lane);
       if (FP8 && !window) {
@@ -1248,8 +1254,7 @@ int sm_count() {
 // splitting only multiplies the items' overhead (and their tokens may be far shorter than
 // L_max says): never.
 int plan_splits(int n_w, int m, int k, int N, int L_max) {
-  const int E = k > 0 ? k : L_max / m;
-  const int tiles = (E + kRows - 1) / kRows + (n_w + kRows - 1) / kRows;
+  const int tiles = tiles_of(k > 0 ? k : L_max / m) + tiles_of(std::max(n_w, 0));
   const int sms = sm_count();
   int best = 1;
   double least = 0;

@@ -166,3 +166,15 @@ def test_binding_checks_types_places_and_sizes():
         L.csa_window_append(L.CSA_F32, 8, 4, torch.zeros(1, 4, 8), torch.zeros(2, 8), None, None, 1, 2)
     with pytest.raises(L.CsaError):
         L.csa_window_append(L.CSA_FP8_E4M3, 8, 4, None, None, None, None, 1, 2)
+
+
+@pytest.mark.parametrize("m", [1, 4])
+def test_workspace_of_the_longest_positions(m):
+    """A bound of 2^31 - 1 positions (or one that only says "any") splits like one a tile shorter."""
+    lib, kv = L.lib(), cache()
+    p = L.AttnParams(H=64, d=512, n_w=128, scale=1.0, m=m, k=0, dtype=L.CSA_BF16)
+    far = 2 ** 31 - 1
+    for N in (1, 8, 150):
+        size, launches = [[f(ctypes.byref(p), ctypes.byref(kv), 1, N, x) for x in (far, far - 128 * m)]
+                          for f in (lib.csa_chunk_attn_workspace_size, lib.csa_chunk_attn_launch_count)]
+        assert size[0] == size[1] > 0 and launches == [2, 2], (N, size, launches)

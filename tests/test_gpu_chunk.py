@@ -856,3 +856,15 @@ def test_a_sequence_served_in_chunks(fmt, m, n):
     assert float(err) <= 2 * 2.0 ** -8 * 2 * A
     # the lse: the whole call sums rounded weights (2^-8 each, relative)
     assert float((torch.cat(lses) - lse[0]).abs().max()) <= 2.0 ** -8 + 2.0 ** -14 * 100
+
+
+@pytest.mark.parametrize("shape", ["tc", "small"])
+@pytest.mark.parametrize("lens", [[1, 1, 3], [2, 150, 160]])
+def test_chunk_attn_last_positions(shape, lens):
+    """Tokens up to position 2^31 - 2, the last one that a bound on t + 1 can name: the ends of
+    their windows' tiles lie past 2^31."""
+    last = 2 ** 31 - 2
+    cfg = dict(TC, fmt=L.CSA_BF16) if shape == "tc" else dict(SMALL)
+    cfg.update(m=2 ** 31 - 1, n_w=140)
+    c = Case(lens, [last + 1 - n for n in lens], k=0, seed=131, **cfg)
+    c.run().check(tokens=5)
