@@ -745,7 +745,8 @@ csa_status csa_qk_norm_rope(const csa_norm_rope_params* p, const void* q, int64_
  *   L_max  bounds t + 1 over the batch; it only sets how the work is split
  *   ws     device scratch of csa_chunk_attn_workspace_size() bytes, 16-byte aligned (NULL
  *          when 0), for this call alone until it has run.  The size depends on the current
- *          device as well as on the arguments.
+ *          device as well as on the arguments; that of smaller arguments can be larger
+ *          (csa_chunk_attn_workspace_bound() covers those too).
  * 64 heads of 512 dims in BF16 over a BF16 cache, or an FP8 one with d_hi = 64, run on the
  * tensor cores (d_rope_out up to 64 there); other shapes on the CUDA cores.
  */
@@ -756,6 +757,14 @@ csa_status csa_chunk_attn(const csa_attn_params* p, const csa_kv_cache* kv, cons
                           void* ws, size_t ws_bytes, cudaStream_t stream);
 size_t csa_chunk_attn_workspace_size(const csa_attn_params* p, const csa_kv_cache* kv, int b, int N,
                                      int L_max);
+/*
+ * Bytes that hold the workspace of every call with up to b sequences, N rows and L_max
+ * positions, for a program that keeps one workspace for all its batches: the size above does
+ * not grow with N and L_max (few tokens are split over the SMs and need partials, many are
+ * not: 16 rows over 1M positions take 18 MB, 148 none, 150 take 94 MB, 296 none).
+ */
+size_t csa_chunk_attn_workspace_bound(const csa_attn_params* p, const csa_kv_cache* kv, int b, int N,
+                                      int L_max);
 /* Number of kernel launches one csa_chunk_attn call makes with these arguments; host only. */
 int csa_chunk_attn_launch_count(const csa_attn_params* p, const csa_kv_cache* kv, int b, int N,
                                 int L_max);

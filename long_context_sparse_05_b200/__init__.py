@@ -10,7 +10,8 @@ built: there is no CPU fallback.
 from ._lib import (CSA_BF16, CSA_F32, CSA_FP8_E4M3, CSA_NVFP4, DTYPE, AttnParams,  # noqa: F401
                    CompressParams, CsaError, DecodeParams, IndexParams, KVCache, NormRopeParams,
                    PrefillParams, alloc_kv_cache, csa_cache_read, csa_cache_write, csa_chunk_attn,
-                   csa_chunk_attn_launch_count, csa_chunk_attn_workspace_size, csa_compress,
+                   csa_chunk_attn_launch_count, csa_chunk_attn_workspace_bound,
+                   csa_chunk_attn_workspace_size, csa_compress,
                    csa_decode, csa_decode_workspace_size, csa_index_scores, csa_prefill,
                    csa_prefill_workspace_size, csa_qk_norm_rope, csa_quantize, csa_sparse_attn,
                    csa_sparse_attn_workspace_size, csa_status_string, csa_topk, csa_window_append,

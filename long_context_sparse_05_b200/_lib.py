@@ -175,6 +175,8 @@ _SIGS = {
                        [c_void_p] * 8 + [c_int] * 3 + [c_void_p] * 3 + [c_size_t, c_void_p]),
     "csa_chunk_attn_workspace_size": (c_size_t, [ctypes.POINTER(AttnParams),
                                                  ctypes.POINTER(KVCache), c_int, c_int, c_int]),
+    "csa_chunk_attn_workspace_bound": (c_size_t, [ctypes.POINTER(AttnParams),
+                                                  ctypes.POINTER(KVCache), c_int, c_int, c_int]),
     "csa_chunk_attn_launch_count": (c_int, [ctypes.POINTER(AttnParams), ctypes.POINTER(KVCache),
                                             c_int, c_int, c_int]),
     "csa_cp_pack_rows": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_int, c_void_p, c_void_p,
@@ -560,6 +562,11 @@ def csa_qk_norm_rope(p, q, q_gain, kv, kv_gain, pos, N, q_out, kv_out, stream=No
 
 def csa_chunk_attn_workspace_size(p, kv, b, N, L_max):
     return int(lib().csa_chunk_attn_workspace_size(ctypes.byref(p), ctypes.byref(kv), b, N, L_max))
+
+
+def csa_chunk_attn_workspace_bound(p, kv, b, N, L_max):
+    """Bytes for every call with up to b sequences, N rows and L_max positions."""
+    return int(lib().csa_chunk_attn_workspace_bound(ctypes.byref(p), ctypes.byref(kv), b, N, L_max))
 
 
 def csa_chunk_attn_launch_count(p, kv, b, N, L_max):

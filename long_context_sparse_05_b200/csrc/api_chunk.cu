@@ -105,6 +105,13 @@ size_t csa_chunk_attn_workspace_size(const csa_attn_params* p, const csa_kv_cach
   return chunk_tc_workspace_bytes(p->n_w, p->m, p->k, N, L_max);
 }
 
+size_t csa_chunk_attn_workspace_bound(const csa_attn_params* p, const csa_kv_cache* kv, int b, int N,
+                                      int L_max) {
+  if (!p || !kv || b <= 0 || N <= 0 || L_max < 1 || p->m < 1) return 0;
+  if (!chunk_tc_supported(p->H, p->d, p->dtype, p->d_rope_out, *kv)) return 0;
+  return chunk_tc_workspace_bound(p->n_w, p->m, p->k, N, L_max);
+}
+
 int csa_chunk_attn_launch_count(const csa_attn_params* p, const csa_kv_cache* kv, int b, int N,
                                 int L_max) {
   if (!p || !kv || b <= 0 || N <= 0 || L_max < 1 || p->m < 1) return 0;

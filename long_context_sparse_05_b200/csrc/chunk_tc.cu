@@ -1253,9 +1253,7 @@ int sm_count() {
 // items each, and the partials of an item about 0.015 in all.  With two tokens per SM or more
 // splitting only multiplies the items' overhead (and their tokens may be far shorter than
 // L_max says): never.
-int plan_splits(int n_w, int m, int k, int N, int L_max) {
-  const int tiles = tiles_of(k > 0 ? k : L_max / m) + tiles_of(std::max(n_w, 0));
-  const int sms = sm_count();
+int splits_for(int tiles, int N, int sms) {
   int best = 1;
   double least = 0;
   if (N >= 2 * sms) return best;
@@ -1265,6 +1263,31 @@ int plan_splits(int n_w, int m, int k, int N, int L_max) {
     if (ns == 1 || cost < least) { best = ns; least = cost; }
   }
   return best;
+}
+// Tiles of a token with L visible positions.
+int token_tiles(int n_w, int m, int k, int L) {
+  return tiles_of(k > 0 ? k : L / m) + tiles_of(std::max(n_w, 0));
+}
+int plan_splits(int n_w, int m, int k, int N, int L_max) {
+  return splits_for(token_tiles(n_w, m, k, L_max), N, sm_count());
+}
+
+// Most items with partials among the calls of up to N tokens and L_max positions.  Every tile
+// count from the first position's to the last's occurs; over kPlanTiles of them (and then they
+// are not tried one by one) all splits may be taken.
+constexpr int kPlanTiles = 4096;
+long long plan_items_bound(int n_w, int m, int k, int N, int L_max) {
+  const int sms = sm_count(), top = std::min(N, 2 * sms - 1);
+  const int first = token_tiles(n_w, m, k, 1), last = token_tiles(n_w, m, k, L_max);
+  if (last > kPlanTiles) return (long long)top * kMaxSplit;
+  long long most = 0;
+  for (int tiles = last; tiles >= first; --tiles) {
+    for (int n = top; n > 0 && (long long)n * std::min(kMaxSplit, tiles) > most; --n) {
+      const int ns = splits_for(tiles, n, sms);
+      if (ns > 1) most = std::max(most, (long long)n * ns);
+    }
+  }
+  return most;
 }
 
 }  // namespace
@@ -1282,6 +1305,10 @@ int chunk_tc_launch_count(int n_w, int m, int k, int N, int L_max) {
 size_t chunk_tc_workspace_bytes(int n_w, int m, int k, int N, int L_max) {
   const int ns = plan_splits(n_w, m, k, N, L_max);
   return ns > 1 ? (size_t)N * ns * kH * (kD + 2) * 4 : 0;
+}
+
+size_t chunk_tc_workspace_bound(int n_w, int m, int k, int N, int L_max) {
+  return (size_t)plan_items_bound(n_w, m, k, N, L_max) * kH * (kD + 2) * 4;
 }
 
 csa_status launch_chunk_attn_tc(const ChunkArgs& a, const csa_kv_cache& kv, void* ws,

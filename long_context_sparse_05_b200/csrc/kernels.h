@@ -194,6 +194,7 @@ csa_status launch_chunk_attn_simt(const ChunkArgs& a, const csa_kv_cache& kv, in
                                   cudaStream_t st);
 bool chunk_tc_supported(int H, int d, int dtype, int d_rope_out, const csa_kv_cache& kv);
 size_t chunk_tc_workspace_bytes(int n_w, int m, int k, int N, int L_max);
+size_t chunk_tc_workspace_bound(int n_w, int m, int k, int N, int L_max);
 int chunk_tc_launch_count(int n_w, int m, int k, int N, int L_max);
 csa_status launch_chunk_attn_tc(const ChunkArgs& a, const csa_kv_cache& kv, void* ws,
                                 size_t ws_bytes, cudaStream_t st);

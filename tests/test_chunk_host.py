@@ -178,3 +178,32 @@ def test_workspace_of_the_longest_positions(m):
         size, launches = [[f(ctypes.byref(p), ctypes.byref(kv), 1, N, x) for x in (far, far - 128 * m)]
                           for f in (lib.csa_chunk_attn_workspace_size, lib.csa_chunk_attn_launch_count)]
         assert size[0] == size[1] > 0 and launches == [2, 2], (N, size, launches)
+
+
+@pytest.mark.parametrize("k,m,n_w", [(0, 128, 128), (0, 4, 128), (512, 4, 128), (0, 4, 0), (4096, 4, 300)])
+def test_workspace_bound_covers_every_smaller_call(k, m, n_w):
+    """One workspace for a program's largest batch and context serves its smaller calls."""
+    lib, kv = L.lib(), cache()
+    p = L.AttnParams(H=64, d=512, n_w=n_w, scale=1.0, m=m, k=k, dtype=L.CSA_BF16)
+    args = ctypes.byref(p), ctypes.byref(kv), 1
+    for N, L_max in ((1, 1), (1, 1 << 14), (16, 1 << 15), (150, 1 << 15), (296, 1 << 15), (5000, 1 << 14)):
+        bound = lib.csa_chunk_attn_workspace_bound(*args, N, L_max)
+        # a context for each number of tiles: E entries, from 0 to the last
+        most = max(lib.csa_chunk_attn_workspace_size(*args, n, x)
+                   for n in range(1, min(N, 300) + 1)
+                   for x in ([L_max] if k else [*range(1, L_max, 128 * m), L_max]))
+        assert bound == most, (N, L_max, bound, most)
+    for far in (1 << 24, 2 ** 31 - 1):               # too many tiles to try each: still a bound
+        bound = lib.csa_chunk_attn_workspace_bound(*args, 296, far)
+        assert all(lib.csa_chunk_attn_workspace_size(*args, n, x) <= bound
+                   for n in range(1, 297) for x in (far, far // 2, far // 3, far // 1000))
+
+
+def test_workspace_bound_of_nothing():
+    f = L.lib().csa_chunk_attn_workspace_bound
+    p = L.AttnParams(H=64, d=512, n_w=128, scale=1.0, m=4, k=0, dtype=L.CSA_BF16)
+    for a in ((0, 4, 64), (1, 0, 64), (1, 4, 0)):
+        assert f(ctypes.byref(p), ctypes.byref(cache()), *a) == 0
+    assert f(None, None, 1, 1, 1) == 0
+    p.H = 32                                         # the CUDA-core kernel takes none
+    assert f(ctypes.byref(p), ctypes.byref(cache()), 1, 8, 1 << 20) == 0

@@ -868,3 +868,20 @@ def test_chunk_attn_last_positions(shape, lens):
     cfg.update(m=2 ** 31 - 1, n_w=140)
     c = Case(lens, [last + 1 - n for n in lens], k=0, seed=131, **cfg)
     c.run().check(tokens=5)
+
+
+def test_one_workspace_for_all_batches():
+    """A workspace for the largest batch and context, used by calls of every smaller size: what a
+    call of its own size's workspace gives."""
+    big = Case([300], [30000], m=4, k=0, seed=141, fmt=L.CSA_BF16, **TC)
+    ws = torch.full((L.csa_chunk_attn_workspace_bound(big.p, big.kv, 3, big.N, big.L_max),), 0xFF,
+                    dtype=torch.uint8, device="cuda")
+    assert ws.numel() > L.csa_chunk_attn_workspace_size(big.p, big.kv, 1, big.N, big.L_max)
+    for lens, ctx in (([300], [30000]), ([1], [30000]), ([1, 1, 1], [20000, 9, 30000]), ([148], [7000]),
+                      ([150], [30000]), ([33, 2], [500, 29000])):
+        c = Case(lens, ctx, m=4, k=0, seed=142, fmt=L.CSA_BF16, **TC).run()
+        out, lse = c.out.clone(), c.lse.clone()
+        c.out.fill_(7.0)
+        c.ws = ws
+        c.run()
+        assert torch.equal(out, c.out) and torch.equal(lse, c.lse), lens
