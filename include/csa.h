@@ -769,6 +769,14 @@ size_t csa_chunk_attn_workspace_bound(const csa_attn_params* p, const csa_kv_cac
 int csa_chunk_attn_launch_count(const csa_attn_params* p, const csa_kv_cache* kv, int b, int N,
                                 int L_max);
 
+/*
+ * Failure-detection self-test: in the calling thread's next csa_chunk_attn on the tensor cores,
+ * the warps of one role (1 softmax and output, 2 loads, 3 the hand-over to the MMAs) act as if
+ * a wait of theirs had given up.  The waits themselves are done, the error word is set, and
+ * the call's out and lse are NaN.
+ */
+csa_status csa_selftest_chunk_give_up(int role);
+
 #ifdef __cplusplus
 }
 #endif

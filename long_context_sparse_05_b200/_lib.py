@@ -177,6 +177,7 @@ _SIGS = {
                                                  ctypes.POINTER(KVCache), c_int, c_int, c_int]),
     "csa_chunk_attn_workspace_bound": (c_size_t, [ctypes.POINTER(AttnParams),
                                                   ctypes.POINTER(KVCache), c_int, c_int, c_int]),
+    "csa_selftest_chunk_give_up": (c_int, [c_int]),
     "csa_chunk_attn_launch_count": (c_int, [ctypes.POINTER(AttnParams), ctypes.POINTER(KVCache),
                                             c_int, c_int, c_int]),
     "csa_cp_pack_rows": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_int, c_void_p, c_void_p,
@@ -232,6 +233,11 @@ def csa_device_error(stream=None):
 
 def csa_selftest_bounded_wait(limit_us, stream=None):
     _check(lib().csa_selftest_bounded_wait(limit_us, _stream(stream)))
+
+
+def csa_selftest_chunk_give_up(role):
+    """The next csa_chunk_attn of this thread acts as if a wait of the role (1..3) had given up."""
+    _check(lib().csa_selftest_chunk_give_up(role))
 
 
 def csa_status_string(status):

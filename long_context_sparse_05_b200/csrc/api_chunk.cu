@@ -119,6 +119,10 @@ int csa_chunk_attn_launch_count(const csa_attn_params* p, const csa_kv_cache* kv
   return chunk_tc_launch_count(p->n_w, p->m, p->k, N, L_max);
 }
 
+csa_status csa_selftest_chunk_give_up(int role) {
+  return chunk_tc_give_up(role) ? CSA_OK : CSA_ERR_INVALID_ARG;
+}
+
 csa_status csa_chunk_attn(const csa_attn_params* p, const csa_kv_cache* kv, const void* q,
                           const int32_t* cu_q, const int32_t* pos0, const int32_t* idx,
                           const int32_t* count, const void* win, const void* new_win,

@@ -49,6 +49,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <utility>
 
 namespace csa {
 
@@ -78,6 +79,8 @@ constexpr int kRegsLaunch = 96;       // 65,536 / 640, whole multiples of 8
 static_assert(kRegsSoftmax <= kRegsLaunch && kRegsProd >= kRegsLaunch && kRegsMma <= kRegsLaunch &&
                   2 * kRegsSoftmax + 2 * kRegsProd + kRegsMma <= 5 * kRegsLaunch, "setmaxnreg shares");
 constexpr uint32_t kHintNs = 64;
+constexpr uint64_t kAfterNs = 100000;  // limit of the waits of a CTA of which one gave up
+constexpr uint64_t kDrainNs = 1000000; // what a CTA leaves for its copies and MMAs in flight then
 constexpr int kSeqCache = 1024;       // sequences whose boundaries are kept in shared memory
 constexpr int kSeqOrder = 64;         // sequences that are taken in order of length
 constexpr int kItemList = 1024;       // items of a CTA that are chosen by load
@@ -97,10 +100,34 @@ struct ChunkTc {
   float *part_o, *part_m, *part_l;   // per item [64][512], [64], [64]
   int* err;
   csa_kv_cache kv;
-  int b, N, n_w, m, k, nsplit, items, order, d_rope_out;
+  int b, N, n_w, m, k, nsplit, items, order, d_rope_out, give_up;
   float scale_log2;
   double inv_freq[kMaxOutRopePairs];
 };
+
+// A wait of one of the CTA's roles.  Once one gives up, `failed` (shared memory) says so before
+// anything that it should have held back happens, and the outputs from there on are NaN; the
+// CTA's later waits stay, with a short limit.
+__device__ __forceinline__ void role_wait(uint64_t* bar, uint32_t parity, int* err, volatile int* failed) {
+  if (tc::mbar_try_wait_hint(bar, parity, kHintNs)) return;
+  const uint64_t t0 = tc::globaltimer();
+  while (!tc::mbar_try_wait_hint(bar, parity, kHintNs)) {
+    const uint64_t dt = tc::globaltimer() - t0;
+    if (dt > kAfterNs && (dt > tc::kWaitLimitNs || *failed)) {
+      *failed = 1;
+      atomicExch(err, CSA_ERR_TIMEOUT);
+      return;
+    }
+  }
+}
+// The self-test: the role that acts as if a wait of its own had given up.
+enum Role { kSoftmaxRole = 1, kProducerRole = 2, kWatchRole = 3 };
+__device__ __forceinline__ void role_start(const ChunkTc& p, int role, volatile int* failed) {
+  if (p.give_up == role) {
+    *failed = 1;
+    atomicExch(p.err, CSA_ERR_TIMEOUT);
+  }
+}
 
 struct Item {
   int tok, part, seq, i0, p0, t, nsel, ne, w0, tb, te;   // part: tok * nsplit + split
@@ -605,6 +632,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
   float* s_sink2 = s_alpha + kH;
   float2* s_rot = reinterpret_cast<float2*>(s_sink2 + kH);   // the output's rotation: sine, cosine
   int* s_flag = reinterpret_cast<int*>(s_rot + kMaxOutRopePairs);
+  volatile int* s_failed = s_flag + 1;            // a wait of this CTA gave up
   uint64_t* bar_s = reinterpret_cast<uint64_t*>(s_flag + 4);
   uint64_t* bar_pv = bar_s + 1;                   // [4]
   uint64_t* bar_full = bar_pv + 4;                // [4]: a pair of the tile is in place
@@ -623,6 +651,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
   if (tid == 0) {
     s_cu[Seqs::kOrdered] = 0;
     s_cu[Seqs::kListed] = -1;
+    *s_failed = 0;
   }
   if (tid < kH) s_sink2[tid] = p.sink[tid] * kLog2e;
   if (tid == 0) {
@@ -733,7 +762,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
     // second warp watches the pairs land and hands each over at a named barrier.  (It cannot
     // run ahead: a pair of the next tile lands after this tile's PV has read its place.)
     if (warp == kSW + kPW + 1) {
-      bool ok = true;
+      role_start(p, kWatchRole, s_failed);
       uint32_t g = 0;
       for (int n = 0, item; (item = item_at(seqs, n)) < p.items; ++n) {
         const Item I = get_item(p, seqs, item, lane);
@@ -741,7 +770,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
         for (int j = I.tb; j < I.te; ++j, ++g) {
 #pragma unroll 1
           for (int mb = 0; mb < 4; ++mb) {
-            ok = ok && tc::mbar_wait_hint(bar_full + mb, g & 1, p.err, kHintNs);
+            role_wait(bar_full + mb, g & 1, p.err, s_failed);
             tc::named_bar_arrive(4 + mb, kBarW);
           }
         }
@@ -753,7 +782,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
     const int w = warp - kSW;
     const int row0 = 16 * w;                       // this warp's rows of a tile
     const int myrow = row0 + (lane & 15);          // the one whose place this lane finds out
-    bool ok = true;
+    role_start(p, kProducerRole, s_failed);
     constexpr int NP = kPairs<FP8>;
     uint4 st[kStage<FP8>];
     uint2 sc = make_uint2(0u, 0u);                 // FP8: the scales of this lane's row, and the
@@ -820,7 +849,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
       // waits for the first and then for the last)
       auto wait_pv = [&](int mb) {
         if (n > 0) {
-          ok = ok && tc::mbar_wait_hint(bar_pv + mb, (n - 1) & 1, p.err, kHintNs);
+          role_wait(bar_pv + mb, (n - 1) & 1, p.err, s_failed);
           tc::tc_fence_after();
         }
       };
@@ -893,7 +922,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
       take();
       if (live && new_q) {
         // the queries in shared memory are read by this tile's S^T for the last time
-        ok = ok && tc::mbar_wait_hint(bar_s, n & 1, p.err, kHintNs);
+        role_wait(bar_s, n & 1, p.err, s_failed);
         tc::tc_fence_after();
         queries();
       }
@@ -907,7 +936,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
     const int h0 = 32 * hf + 2 * (lane & 3);       // ... and heads h0 + 8 g, h0 + 8 g + 1, g < 4
     const int row = qd * 32 + lane;                // its TMEM lane of O^T
     uint32_t ns = 0;                               // tiles so far
-    bool ok = true;
+    role_start(p, kSoftmaxRole, s_failed);
 
     for (int n = 0, item; (item = item_at(seqs, n)) < p.items; ++n) {
       const Item I = get_item(p, seqs, item, lane);
@@ -917,7 +946,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
 #pragma unroll
       for (int h = 0; h < 8; ++h) lsum[h] = ref[h] = 0.f;
       for (int j = I.tb; j < I.te; ++j) {
-        ok = ok && tc::mbar_wait_hint(bar_s, ns & 1, p.err, kHintNs);
+        role_wait(bar_s, ns & 1, p.err, s_failed);
         ++ns;
         tc::tc_fence_after();
         const uint32_t have = s_valid[qd];
@@ -1093,7 +1122,8 @@ __global__ void __launch_bounds__(kLaunch, 1)
         // lanes are neighbouring dims: a head's 32 dims leave as one 128-byte line
 #pragma unroll 1
         for (int mb = 0; mb < 4; ++mb) {
-          ok = ok && tc::mbar_wait_hint(bar_pv + mb, (ns - 1) & 1, p.err, kHintNs);
+          role_wait(bar_pv + mb, (ns - 1) & 1, p.err, s_failed);
+          const bool ok = !*s_failed;
           tc::tc_fence_after();
           uint32_t o[32];
           tc::tmem_ld32(tO + mb * kH + 32 * hf + lane_addr, o);
@@ -1118,7 +1148,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
         const int rope0 = kD - p.d_rope_out;
 #pragma unroll 1
         for (int mb = 0; mb < 4; ++mb) {
-          ok = ok && tc::mbar_wait_hint(bar_pv + mb, (ns - 1) & 1, p.err, kHintNs);
+          role_wait(bar_pv + mb, (ns - 1) & 1, p.err, s_failed);
           tc::tc_fence_after();
           uint32_t ob[2][16];
           tmem_ld16x2(tO + mb * kH + 32 * hf + lane_addr, ob);
@@ -1154,7 +1184,8 @@ __global__ void __launch_bounds__(kLaunch, 1)
             }
           }
           // the stage is free: the last PV has read P^T, the store of the block before its rows
-          if (mb == 0) ok = ok && tc::mbar_wait_hint(bar_pv + 3, (ns - 1) & 1, p.err, kHintNs);
+          if (mb == 0) role_wait(bar_pv + 3, (ns - 1) & 1, p.err, s_failed);
+          const bool ok = !*s_failed;
           if (lane == 0) tma_store_wait_read();
           __syncwarp();
 #pragma unroll
@@ -1175,6 +1206,10 @@ __global__ void __launch_bounds__(kLaunch, 1)
       }
       tc::tc_fence_before();
       tc::named_bar(3, kST);                       // s_red, s_alpha and s_M are free again
+      if (tid < kH && *s_failed) {
+        if (p.nsplit > 1) p.part_l[(long long)I.part * kH + tid] = nan_f();   // the merge's output and lse
+        else if (p.lse) p.lse[(long long)I.tok * kH + tid] = nan_f();
+      }
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
@@ -1182,6 +1217,10 @@ __global__ void __launch_bounds__(kLaunch, 1)
   tc::tc_fence_before();
   __syncthreads();
   if (warp == 0) {
+    if (*s_failed) {
+      const uint64_t t0 = tc::globaltimer();
+      while (tc::globaltimer() - t0 < kDrainNs) {}
+    }
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, 512);
   }
@@ -1240,6 +1279,8 @@ __global__ void __launch_bounds__(128 * kMergeHeads) chunk_merge_kernel(const __
 constexpr size_t kSmem = 1024 + 8 * kKVBlk + 8 * kQBlk + kRows * 128 + (4 * kH + 3 * kH) * 4 + kMaxOutRopePairs * 8 + 16 + 9 * 8 + 8 + 16 +
                          Seqs::kWords * 4;
 static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+
+thread_local int t_give_up = 0;   // csa_selftest_chunk_give_up: of this thread's next call
 
 int sm_count() {
   int dev = 0, sms = 148;
@@ -1311,6 +1352,12 @@ size_t chunk_tc_workspace_bound(int n_w, int m, int k, int N, int L_max) {
   return (size_t)plan_items_bound(n_w, m, k, N, L_max) * kH * (kD + 2) * 4;
 }
 
+bool chunk_tc_give_up(int role) {
+  if (role < kSoftmaxRole || role > kWatchRole) return false;
+  t_give_up = role;
+  return true;
+}
+
 csa_status launch_chunk_attn_tc(const ChunkArgs& a, const csa_kv_cache& kv, void* ws,
                                 size_t ws_bytes, cudaStream_t st) {
   // row numbers of the window and of q carry a tag in bit 30
@@ -1322,6 +1369,7 @@ csa_status launch_chunk_attn_tc(const ChunkArgs& a, const csa_kv_cache& kv, void
   p.cu_q = a.cu_q; p.pos0 = a.pos0; p.idx = a.idx; p.count = a.count; p.sink = a.sink;
   p.out = static_cast<__nv_bfloat16*>(a.out); p.lse = a.lse; p.kv = kv;
   p.b = a.b; p.N = a.N; p.n_w = a.n_w; p.m = a.m; p.k = a.k; p.d_rope_out = a.d_rope_out;
+  p.give_up = std::exchange(t_give_up, 0);
   p.scale_log2 = a.scale * kLog2e;
   p.err = device_error_word();
   if (!p.err) return CSA_ERR_CUDA;

@@ -196,6 +196,9 @@ bool chunk_tc_supported(int H, int d, int dtype, int d_rope_out, const csa_kv_ca
 size_t chunk_tc_workspace_bytes(int n_w, int m, int k, int N, int L_max);
 size_t chunk_tc_workspace_bound(int n_w, int m, int k, int N, int L_max);
 int chunk_tc_launch_count(int n_w, int m, int k, int N, int L_max);
+// Lets the named role (1 softmax, 2 loads, 3 the warp that watches them) of this thread's next
+// launch_chunk_attn_tc act as if one of its waits had given up; false if there is no such role.
+bool chunk_tc_give_up(int role);
 csa_status launch_chunk_attn_tc(const ChunkArgs& a, const csa_kv_cache& kv, void* ws,
                                 size_t ws_bytes, cudaStream_t st);
 

@@ -207,3 +207,8 @@ def test_workspace_bound_of_nothing():
     assert f(None, None, 1, 1, 1) == 0
     p.H = 32                                         # the CUDA-core kernel takes none
     assert f(ctypes.byref(p), ctypes.byref(cache()), 1, 8, 1 << 20) == 0
+
+
+def test_give_up_refusals():
+    f = L.lib().csa_selftest_chunk_give_up
+    assert f(0) == INVALID and f(4) == INVALID and f(-1) == INVALID

@@ -885,3 +885,21 @@ def test_one_workspace_for_all_batches():
         c.ws = ws
         c.run()
         assert torch.equal(out, c.out) and torch.equal(lse, c.lse), lens
+
+
+@pytest.mark.parametrize("fmt,d_hi", [(L.CSA_BF16, 0), (L.CSA_FP8_E4M3, 64)])
+@pytest.mark.parametrize("role", [1, 2, 3])
+@pytest.mark.parametrize("lens,ctx,k", [([5, 3], [2500, 900], 0), ([5, 3], [2500, 900], 64), ([310, 40], [700, 0], 0)])
+def test_chunk_attn_a_wait_given_up(fmt, d_hi, role, lens, ctx, k):
+    """Whichever warps' wait gives up: the error word is set and the outputs are NaN, never silently
+    wrong; the next call is right again."""
+    assert L.csa_device_error() == 0
+    c = Case(lens, ctx, m=4, k=k, seed=151, fmt=fmt, d_hi=d_hi, d_rope_out=64, **TC)
+    n = c.cu[-1]
+    L.csa_selftest_chunk_give_up(role)
+    with pytest.raises(AssertionError):
+        c.run()                                      # (its own look at the error word)
+    assert L.csa_device_error() == 0
+    assert torch.all(torch.isnan(c.out[:n])) and torch.all(torch.isnan(c.lse[:n]))
+    assert torch.all(c.out[n:] == 7.0) and torch.all(c.lse[n:] == 7.0)
+    c.run().check(tokens=3)
