@@ -941,7 +941,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
     for (int n = 0, item; (item = item_at(seqs, n)) < p.items; ++n) {
       const Item I = get_item(p, seqs, item, lane);
       if (!I.live) break;
-      bool started = false;                        // a tile of this item had a row
+      bool open = true;                            // some head has no maximum yet: no row, or only -inf
       float lsum[8], ref[8];                       // sums, and reference maxima (log2 units, 0: none)
 #pragma unroll
       for (int h = 0; h < 8; ++h) lsum[h] = ref[h] = 0.f;
@@ -972,8 +972,8 @@ __global__ void __launch_bounds__(kLaunch, 1)
           }
         };
         logits();
-        // the item's first tile, and any up to the first with a row, set the maximum
-        bool exact = !started;
+        // the item's first tile, and any while a head has no maximum, set it
+        bool exact = open;
         if (!exact) {
           float top = -INFINITY;
 #pragma unroll
@@ -981,7 +981,6 @@ __global__ void __launch_bounds__(kLaunch, 1)
           exact = tc::bar_red_or(3, kST, top > kRescale);
         }
         if (exact) {
-          const bool rows = (s_valid[0] | s_valid[1] | s_valid[2] | s_valid[3]) != 0;
           float v[8];
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
@@ -997,7 +996,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
 #pragma unroll
             for (int h = 0; h < 8; ++h) v[h] = fmaxf(v[h], __shfl_xor_sync(0xffffffffu, v[h], o));
           }
-          if (tid == 0) s_flag[0] = 0;             // its last reads are behind a barrier
+          if (tid == 0) s_flag[0] = s_flag[2] = 0;   // their last reads are behind a barrier
           if (lane == 0) tma_store_wait_read();    // an item's first P^T comes after this and the barrier
           if (lane < 4) {
 #pragma unroll
@@ -1008,10 +1007,11 @@ __global__ void __launch_bounds__(kLaunch, 1)
           if (tid < kH) {
             // this tile's maxima, relative to the reference that the logits were taken against
             const float tm = fmaxf(fmaxf(s_red[tid], s_red[kH + tid]), fmaxf(s_red[2 * kH + tid], s_red[3 * kH + tid]));
-            // (rows whose logits are all -inf are taken against 0: they weigh nothing)
-            float Mn = started ? s_M[tid] : rows && tm == -INFINITY ? 0.f : tm;
-            float al = started ? 1.f : 0.f;
-            if (started && tm > kRescale) {
+            float Mn = j > I.tb ? s_M[tid] : -INFINITY, al = 1.f;
+            if (Mn == -INFINITY) {                 // its first: the logits were taken against 0
+              Mn = tm;
+              if (tm == -INFINITY) s_flag[2] = 1;
+            } else if (tm > kRescale) {
               Mn += tm;
               al = exp2f(-tm);
               s_flag[0] = 1;
@@ -1020,7 +1020,7 @@ __global__ void __launch_bounds__(kLaunch, 1)
             s_alpha[tid] = al;
           }
           tc::named_bar(3, kST);
-          if (started && s_flag[0]) {
+          if (s_flag[0]) {
 #pragma unroll 1
             for (int y = 0; y < 4; ++y) {          // this half's two dim blocks, 32 heads each time
               uint32_t o[32];
@@ -1041,12 +1041,12 @@ __global__ void __launch_bounds__(kLaunch, 1)
           for (int g = 0; g < 4; ++g) {
             const float2 M2 = *reinterpret_cast<const float2*>(s_M + h0 + 8 * g);
             const float2 a2 = *reinterpret_cast<const float2*>(s_alpha + h0 + 8 * g);
-            ref[2 * g] = M2.x == -INFINITY ? 0.f : M2.x;   // a tile without rows gives p = 0, not NaN
+            ref[2 * g] = M2.x == -INFINITY ? 0.f : M2.x;   // nothing but -inf gives p = 0, not NaN
             ref[2 * g + 1] = M2.y == -INFINITY ? 0.f : M2.y;
             lsum[2 * g] *= a2.x;
             lsum[2 * g + 1] *= a2.y;
           }
-          started = started || rows;               // rows are masked for all heads alike
+          open = s_flag[2] != 0;
           logits();
           // nobody may overwrite these maxima before everyone has read them
           tc::named_bar(3, kST);

@@ -903,3 +903,43 @@ def test_chunk_attn_a_wait_given_up(fmt, d_hi, role, lens, ctx, k):
     assert torch.all(torch.isnan(c.out[:n])) and torch.all(torch.isnan(c.lse[:n]))
     assert torch.all(c.out[n:] == 7.0) and torch.all(c.lse[n:] == 7.0)
     c.run().check(tokens=3)
+
+
+@pytest.mark.parametrize("fmt,d_hi", [(L.CSA_BF16, 0), (L.CSA_FP8_E4M3, 64)])
+@pytest.mark.parametrize("lens,ctx", [([300], [2500]), ([5, 3], [2500, 900])])
+def test_chunk_attn_a_head_that_starts_with_infinities(fmt, d_hi, lens, ctx):
+    """Head 0's logits are -inf (past float32) on the first 128 entries and all the same far
+    negative number on the other rows: it weighs those alike, however low they lie."""
+    c = Case(lens, ctx, m=4, k=0, seed=161, fmt=fmt, d_hi=d_hi, sink=-math.inf, **TC)
+    big, low = 3.0e38, 4096.0
+    pool = randn(162, (c.kv.num_pages * PE, c.d))
+    pool[:, 0], pool[:, 100] = 0.0, 1.0
+    for s in range(c.b):
+        for e in range(128):
+            pool[place(c.bt, s, e), :64] = 0.0
+            pool[place(c.bt, s, e), 0] = big
+    flat = L.kv_cache(fmt, c.d, d_hi, *c.kv._tensors[:3], i32([list(range(c.kv.num_pages))]))
+    L.csa_cache_write(flat, L.CSA_F32, pool, i32([0, len(pool)]), i32([0]), 1, len(pool))
+    for w in (c.win, c.new_win):
+        w[..., 0], w[..., 100] = 0.0, 1.0
+    c.q[:, :, 0] = 0.0
+    c.q[:, 0] = 0.0
+    c.q[:, 0, 0], c.q[:, 0, 100] = -big, -low
+    c.run()
+    c.rows64 = c.values()
+    win, nw = f64(c.win), f64(c.new_win)
+    # (the other heads' sums of 3e38 in dim 0, not yet divided by the denominator, pass float32)
+    assert torch.all(torch.isfinite(c.out[:c.cu[-1], 0].float())) and torch.all(torch.isfinite(c.out[:c.cu[-1], :, 1:].float()))
+    for s in range(c.b):
+        for i in {0, 1, lens[s] - 1}:
+            _, rows = chunk.chunk_rows(s, i, c.entry, None, ctx[s], c.cu[s], 4, c.bt.shape[1] * PE, win, nw, 128)
+            rows = np.asarray(rows)
+            seen = rows[rows[:, 0] == 0.0]
+            assert len(rows) == len(seen) + 128
+            logit = -low * c.p.scale * seen[0, 100]
+            # equal weights: one sum of R rows, and the result's rounding; the lse as in check()
+            tol = 2.0 ** -8 * np.abs(seen.mean(0)) + len(seen) * 2.0 ** -23 * np.abs(seen).mean(0)
+            row = c.cu[s] + i
+            assert np.all(np.abs(f64(c.out[row, 0]) - seen.mean(0)) <= tol + 1e-30), (s, i)
+            lse = logit + math.log(len(seen))
+            assert abs(float(c.lse[row, 0]) - lse) <= abs(logit) * 2.0 ** -14 + 2.0 ** -20 + 2.0 ** -22 * abs(lse)
