@@ -416,7 +416,6 @@ def _plain(dtype):
 
 
 _BYTES = (torch.uint8, torch.float8_e4m3fn)
-_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _place(stream):
@@ -425,7 +424,8 @@ def _place(stream):
         raise CsaError("tensor arguments must be CUDA tensors, and there is no CUDA device")
     dev = torch.cuda.current_device()
     if stream is None:
-        return dev, _raw_stream(dev)
+        # (taken here: a build of torch without CUDA lacks it, and imports this file all the same)
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
     if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
         raise CsaError("the stream is on %s, not on the current device" % stream.device)
     return dev, _stream(stream)

@@ -4,6 +4,7 @@ errors that come back before any launch (fake pointers are never dereferenced)."
 import ctypes
 import os
 import subprocess
+import sys
 import tempfile
 
 import pytest
@@ -212,3 +213,22 @@ def test_workspace_bound_of_nothing():
 def test_give_up_refusals():
     f = L.lib().csa_selftest_chunk_give_up
     assert f(0) == INVALID and f(4) == INVALID and f(-1) == INVALID
+
+
+def test_the_package_imports_on_a_torch_without_cuda():
+    """Such a build lacks the private CUDA functions of torch._C; the calls then say what is missing."""
+    code = """
+import torch
+for n in [n for n in dir(torch._C) if n.startswith("_cuda_")]:
+    delattr(torch._C, n)
+torch.cuda.is_available = torch.cuda.is_initialized = lambda: False
+import long_context_sparse_05_b200 as csa
+t = torch.zeros(1, 4, 8)
+try:
+    csa.csa_window_append(csa.CSA_F32, 8, 4, t, t[0], t, t, 1, 2)
+except csa.CsaError as e:
+    print("refused:", e)
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.startswith("refused:") and "CUDA" in r.stdout
