@@ -943,3 +943,103 @@ def test_chunk_attn_a_head_that_starts_with_infinities(fmt, d_hi, lens, ctx):
             assert np.all(np.abs(f64(c.out[row, 0]) - seen.mean(0)) <= tol + 1e-30), (s, i)
             lse = logit + math.log(len(seen))
             assert abs(float(c.lse[row, 0]) - lse) <= abs(logit) * 2.0 ** -14 + 2.0 ** -20 + 2.0 ** -22 * abs(lse)
+
+
+# -------------------------------------------------------- calls large enough for several rows per warp
+
+@pytest.mark.parametrize("dtype,d,d_rope", [
+    (L.CSA_BF16, 128, 64), (L.CSA_F32, 128, 64), (L.CSA_BF16, 256, 0), (L.CSA_F32, 40, 6), (L.CSA_F32, 512, 64),
+    (L.CSA_BF16, 1000, 64), (L.CSA_F32, 1024, 128), (L.CSA_BF16, 2048, 64), (L.CSA_F32, 1800, 64),
+])
+@pytest.mark.parametrize("norm", [0, 1])
+def test_norm_rope_many_rows(dtype, d, d_rope, norm):
+    """Enough rows for several per warp, with a rest: within the oracle's bound, and the same bits as
+    calls of few tokens (the same operations in the same order)."""
+    N, H = 6401, 2
+    test_norm_rope(dtype, N, H, d, d_rope, bool(norm), True, norm)
+    dt = TDT[dtype]
+    q, kv = randn(171, (N, H, d), dt), randn(172, (N, d), dt)
+    g = 1 + 0.2 * randn(173, (d,)) if norm else None
+    pos = torch.arange(N, dtype=torch.int32, device="cuda") * 163
+    p = L.NormRopeParams(H=H, d=d, d_rope=d_rope, rope_theta=THETA, eps=EPS, apply_norm=norm, dtype=dtype)
+    for use_q, use_kv in ((True, True), (False, True)) if d == 128 else ((True, True),):
+        n = N if use_q else 4 * N
+        if not use_q:
+            kv, pos = randn(174, (n, d), dt), torch.arange(n, dtype=torch.int32, device="cuda")
+        outs = []
+        for step in (n, 1000):
+            qo = torch.full_like(q, 7.0) if use_q else None
+            ko = torch.full_like(kv, 7.0)
+            for a in range(0, n, step):
+                z = min(a + step, n)
+                L.csa_qk_norm_rope(p, q[a:z] if use_q else None, g if use_q else None, kv[a:z], g, pos[a:z], z - a,
+                                   qo[a:z] if use_q else None, ko[a:z])
+            outs.append((qo, ko))
+        assert torch.equal(outs[0][1], outs[1][1])
+        assert not use_q or torch.equal(outs[0][0], outs[1][0])
+
+
+@pytest.mark.parametrize("x_dtype,c,d_hi,lens,first", [
+    (L.CSA_F32, 512, 64, [39000, 77], [0, 9]),
+    (L.CSA_BF16, 1104, 16, [12, 37999, 0, 1], [250, 3, 0, 0]),
+    (L.CSA_F32, 64, 0, [1, 38001], [0, 255]),
+])
+def test_cache_write_many_rows(x_dtype, c, d_hi, lens, first):
+    test_cache_write_and_read(L.CSA_FP8_E4M3, x_dtype, c, d_hi, lens, first)
+
+
+@pytest.mark.parametrize("c,d_hi", [(512, 64), (1104, 16), (64, 0)])
+@pytest.mark.parametrize("out_dtype", [L.CSA_BF16, L.CSA_F32])
+def test_cache_read_many_rows(c, d_hi, out_dtype):
+    """An odd number of slots, enough for two rows per warp, whose pairs mix rows that exist with
+    ones past a count, past the table and on pages outside the pool: what reads of few slots give."""
+    b, k, entries = 3, 13001, 700
+    total, bt = table([entries] * b, seed=181, extra=2)
+    bt[1, 1] = total + 5
+    kv = cache_of(L.CSA_FP8_E4M3, c, d_hi, total, bt)
+    flat = L.kv_cache(L.CSA_FP8_E4M3, c, d_hi, *kv._tensors[:3], i32([list(range(total))]))
+    pool = randn(182, (total * PE, c))
+    L.csa_cache_write(flat, L.CSA_F32, pool, i32([0, total * PE]), i32([0]), 1, total * PE)
+    rng = np.random.default_rng(183)
+    idx = torch.from_numpy(rng.integers(-40, entries + 400, (b, k)).astype(np.int32)).cuda()
+    for sel, counts in ((idx, [k, 12345, 1]), (idx, None), (None, [k, 601, 0])):
+        count = None if counts is None else i32(counts)
+        out = torch.full((b, k, c), float("nan"), dtype=TDT[out_dtype], device="cuda")
+        L.csa_cache_read(kv, sel, count, b, k, out_dtype, out)
+        assert not torch.isnan(out).any()
+        step = 5000 if sel is not None else k        # (entry j of slot j: a slice starts at 0 again)
+        for s in range(b):
+            part = L.kv_cache(L.CSA_FP8_E4M3, c, d_hi, *kv._tensors[:3], i32([bt[s].tolist()]))
+            for a in range(0, k, step):
+                z = min(a + step, k)
+                want = torch.empty((1, z - a, c), dtype=TDT[out_dtype], device="cuda")
+                n = None if counts is None else i32([min(max(counts[s] - a, 0), z - a)])
+                L.csa_cache_read(part, None if sel is None else sel[s:s + 1, a:z].contiguous(), n, 1, z - a, out_dtype, want)
+                assert torch.equal(out[s, a:z], want[0]), (s, a)
+    # a sample of the last read's rows against the oracle
+    arrs = [None if t is None else t.cpu() for t in kv._tensors[:3]]
+    L.csa_cache_read(kv, idx, None, b, k, out_dtype, out)
+    for s in range(b):
+        for j in (0, 1, 2, k // 2, k - 2, k - 1):
+            e = int(idx[s, j])
+            if not (0 <= e < bt.shape[1] * PE and 0 <= bt[s, e // PE] < total):
+                assert torch.all(out[s, j] == 0)
+                continue
+            at = place(bt, s, e)
+            hi = f64(arrs[1][at]) if d_hi else np.zeros(0)
+            ref = chunk.dequant_row(arrs[0][at].numpy(), hi, arrs[2][at].numpy()[: (c - d_hi) // 64])
+            assert np.array_equal(f64(out[s, j]), ref), (s, j, e)
+
+
+@pytest.mark.parametrize("fmt,d_hi,shape", [(L.CSA_BF16, 0, "tc"), (L.CSA_FP8_E4M3, 64, "tc"), (L.CSA_F32, 0, "small")])
+@pytest.mark.parametrize("lens,ctx,k", [([5, 3], [2500, 900], 0), ([310, 4], [2500, 900], 64), ([310, 4], [2500, 90], 0)])
+def test_chunk_attn_repeats_itself(fmt, d_hi, shape, lens, ctx, k):
+    """The same call gives the same bits every time (no sum depends on the order of arrival)."""
+    cfg = dict(TC, m=4) if shape == "tc" else dict(SMALL)
+    cfg["fmt"] = fmt
+    c = Case(lens, ctx, k=k, d_hi=d_hi, seed=191, **cfg).run()
+    out, lse = c.out.clone(), c.lse.clone()
+    for _ in range(10):
+        c.out.fill_(7.0)
+        c.run()
+        assert torch.equal(out, c.out) and torch.equal(lse, c.lse)
