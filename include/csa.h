@@ -625,7 +625,9 @@ csa_status csa_cp_pack_rows(const void* kv_local, int E_cap_local, int E_local, 
 /*
  * A serving step brings every sequence a chunk of new tokens: one (decode), a few
  * (drafted tokens to verify) or many (a piece of a prompt).  The calls below are such a
- * step's parts around the compressor, the indexer and the top-k:
+ * step's parts around the compressor, the indexer and the top-k (which take their own
+ * layouts: csa_compress and csa_index_scores no ragged batch and no pages; csa_decode_paged
+ * plain pages alone):
  *
  *   csa_qk_norm_rope    the query heads and the token's latent row, normalised and rotated;
  *   csa_cache_write     compressed entries into their pages, quantised if the cache is;
@@ -743,12 +745,17 @@ csa_status csa_qk_norm_rope(const csa_norm_rope_params* p, const void* q, int64_
  *   win [b][n_w][d] (both NULL iff n_w = 0), sink [H] (-inf: no sink), out [N][H][d],
  *   lse [N][H] float32 or NULL
  *   L_max  bounds t + 1 over the batch; it only sets how the work is split
+ *   N      too decides on that (from two tokens per SM on, none is split): a bound far above
+ *          cu_q[b] leaves few tokens of a long context on as many SMs as there are tokens
  *   ws     device scratch of csa_chunk_attn_workspace_size() bytes, 16-byte aligned (NULL
  *          when 0), for this call alone until it has run.  The size depends on the current
  *          device as well as on the arguments; that of smaller arguments can be larger
  *          (csa_chunk_attn_workspace_bound() covers those too).
  * 64 heads of 512 dims in BF16 over a BF16 cache, or an FP8 one with d_hi = 64, run on the
- * tensor cores (d_rope_out up to 64 there); other shapes on the CUDA cores.
+ * tensor cores (d_rope_out up to 64 there); other shapes on the CUDA cores.  Logits, softmax
+ * sums and outputs are accumulated in float32 (the output before its division by the sum: rows
+ * whose weighted sum passes float32 give infinities).  On the tensor cores each weight is
+ * rounded to BF16 before it multiplies its row, not in the sum and the lse.
  */
 csa_status csa_chunk_attn(const csa_attn_params* p, const csa_kv_cache* kv, const void* q,
                           const int32_t* cu_q, const int32_t* pos0, const int32_t* idx,
@@ -761,7 +768,8 @@ size_t csa_chunk_attn_workspace_size(const csa_attn_params* p, const csa_kv_cach
  * Bytes that hold the workspace of every call with up to b sequences, N rows and L_max
  * positions, for a program that keeps one workspace for all its batches: the size above does
  * not grow with N and L_max (few tokens are split over the SMs and need partials, many are
- * not: 16 rows over 1M positions take 18 MB, 148 none, 150 take 94 MB, 296 none).
+ * not: with m = 128 on 148 SMs, 16 rows over 1M positions take 18 MB, 148 none, 150 take
+ * 94 MB, 296 none).
  */
 size_t csa_chunk_attn_workspace_bound(const csa_attn_params* p, const csa_kv_cache* kv, int b, int N,
                                       int L_max);

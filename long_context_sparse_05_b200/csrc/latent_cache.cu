@@ -7,13 +7,16 @@
 // per 64 dims, so that a code is one rounding of the value and code times scale is exact in
 // bf16, and the rotary dims left in bf16.
 //
-// Memory bound: a quantised row of 512 dims is 584 bytes (448 codes, 64 bf16 dims, 7 scale
+// Bound by memory, the quantised kernels by instruction issue as well (67 to 77 % of the slots
+// active): a quantised row of 512 dims is 584 bytes (448 codes, 64 bf16 dims, 7 scale
 // exponents) against 1024 in bf16.  A warp owns a row: lane l takes 16 consecutive dims, so
 // 512 dims are one pass of the warp, a scale group is four neighbouring lanes (two shuffles
 // for its maximum) and codes leave as 16-byte stores.  Large calls take two rows per warp,
 // both loaded before the first is used, with registers held to five CTAs an SM.  262,144 rows
-// of 512 (421 MB): written 78 us, read back 79 us, 5.4 TB/s (four rows per warp 82 and 87 us,
-// one 82 and 99); 16 rows 2.3 us, a selection of 16 x 512 rows 4.9 us.
+// of 512 (421 MB): written 84 us, read back 80 us, 5.0 and 5.3 TB/s (four rows per warp 4 and 8 us
+// more, one 4 and 20); 16 rows 2.3 us, a selection of 16 x 512 rows 4.9 us.  The same rows from
+// float32 145 us, to float32 154 (690 MB).  Plain rows take one warp each: bf16 98 and 96 us
+// (537 MB), float32 165 and 164 (1.07 GB, 6.5 TB/s).
 #include "chunk_common.cuh"
 
 namespace csa {

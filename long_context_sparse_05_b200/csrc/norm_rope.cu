@@ -3,16 +3,19 @@
 // Method: "DeepSeek V4 结构速览", section "HCA（c128a 路线）" (RMSNorm per head, RoPE on the
 // last dims); the rotation and its float64 angle are the compressor's.
 //
-// Memory bound: every element is read once and written once (2 x 2 bytes in bf16), and the
-// arithmetic per row is one sum of squares.  A warp owns whole rows (a head, or the latent
-// row), kept in registers between the sum and the store: chunks of 8 elements, chunk
+// Every element is read once and written once (2 x 2 bytes in bf16), and the arithmetic per row
+// is one sum of squares and a scaling, which at this byte rate nearly fills the issue slots (76 %
+// of them active, DRAM 55 %).  A warp owns whole rows (a head, or the latent row), kept in registers between the sum and the store: chunks of 8 elements, chunk
 // lane + 32 i.  The rotary angles depend on the token only: the warp forms each pair's sine
 // and cosine once per token (a float64 angle and one sincosf per lane) in its own piece of
 // shared memory and every row of the token takes them from there.  Long inputs take four
 // consecutive rows per warp, all loaded before the first is summed, with registers held to
 // four CTAs an SM; short ones (too few rows for that to fill the SMs) take one.  4096 tokens
-// of 64 heads of 512 (545 MB): 109 us, 5.0 TB/s (one row per warp 137 us, two 114, four
-// without the register bound 117); 16 tokens: 3.2 us.
+// of 64 heads of 512 (545 MB): 109 to 114 us, 4.8 to 5.0 TB/s (beside 109: one row per warp 137 us,
+// two 114, four without the register bound 117); 16 tokens: 3.2 us.  Index queries, 64 heads of
+// 128, leave half of a warp's lanes idle: 78 us for 136 MB.  float32: 252 us for 1.09 GB at 512
+// dims (four rows just pass the 64 registers: 276 bytes a thread are spilled), 84 us for 273 MB
+// at 128.
 
 #include "chunk_common.cuh"
 
