@@ -1043,3 +1043,17 @@ def test_chunk_attn_repeats_itself(fmt, d_hi, shape, lens, ctx, k):
         c.out.fill_(7.0)
         c.run()
         assert torch.equal(out, c.out) and torch.equal(lse, c.lse)
+
+
+@pytest.mark.parametrize("k", [0, 70])
+@pytest.mark.parametrize("over", [
+    dict(H=3, d=136), dict(H=2, d=256, d_rope_out=64), dict(H=2, d=1000, n_w=70),
+    dict(H=16, d=512, dtype=L.CSA_BF16, fmt=L.CSA_BF16, d_rope_out=64),
+    dict(H=16, d=512, dtype=L.CSA_BF16, fmt=L.CSA_FP8_E4M3, d_hi=64, d_rope_out=64),
+    dict(H=64, d=512, dtype=L.CSA_BF16, fmt=L.CSA_BF16, d_rope_out=128),    # more rotary dims than the tensor cores' form
+    dict(H=5, d=576, fmt=L.CSA_FP8_E4M3, d_hi=64, d_rope_out=64),
+])
+def test_chunk_attn_any_shape_wide_heads(k, over):
+    """Head dims past 128, where a thread of the CUDA-core kernel takes one or several channels alone."""
+    cfg = dict(SMALL, **over)
+    Case([4, 0, 1, 17], [0, 9, 1027, 300], k=k, seed=201, **cfg).run().check()
